@@ -1,0 +1,583 @@
+// dense.cuh -- dense matrix products on tcgen05 for any sizes: the gated
+// feed-forward block (forward and backward) and the 8-bit integer product.
+//
+// Every product is D[m][n] = sum_k A(m, k) B(n, k) with fp32 (int32 for int8)
+// accumulators in tensor memory.  An operand is read as it lies in memory:
+// "K-major" (k consecutive) or "MN-major" (m or n consecutive), so neither
+// weights nor activations are transposed or packed beforehand:
+//   gate/up   A = x [T][H]  K-major    B = W_gate, W_up [H][I]  MN-major
+//   down      A = h [T][I]  K-major    B = W_down [I][H]        MN-major
+//   d h       A = dy [T][H] K-major    B = W_down [I][H]        K-major
+//   d x       A = dg, du [T][I] K-major  B = W_gate, W_up [H][I] K-major (two k segments)
+//   d W       A = x, x, h   MN-major   B = dg, du, dy           MN-major (three products)
+//   int8      A = a [T][K]  K-major    B = b [N][K]             K-major
+// A k-block is 128 bytes of k (64 16-bit or 128 8-bit elements).  In shared
+// memory a K-major operand is rows of 128 bytes with the 128-byte swizzle; an
+// MN-major one is chunks of 64 m (or n), each 64 k-rows of 128 bytes, same
+// swizzle.  TMA fills what lies outside the matrix with zeros, in both
+// operands, so ragged sizes need no masks before the store.
+//
+// pair_gemm_kernel: two CTAs of a cluster work on one 256 x BN tile
+// (tcgen05.mma.cta_group::2): each loads 128 rows of A and BN/2 rows of B and
+// holds the accumulators of its 128 rows, so a byte of B in shared memory
+// feeds twice the MMAs of a single-CTA tile.  Persistent, tiles round-robin;
+// two accumulator sets, so the epilogue of one tile overlaps the next one's
+// MMAs.
+#pragma once
+#include "common.cuh"
+
+namespace moe {
+namespace dense {
+
+constexpr unsigned kSiteEmpty = 40, kSiteFull = 41, kSiteTmemFull = 42, kSiteTmemEmpty = 43,
+                   kSiteDrain = 44, kSiteSmallFull = 45, kSiteSmallEmpty = 46, kSiteSmallDone = 47;
+
+enum Kind { kF16Kind = 0, kI8Kind = 1 };                 // operand width: 16 or 8 bits
+enum Epi { kGated = 0, kPlain = 1, kDGate = 2, kScaled = 3 };
+enum Type { kBF16 = 0, kF16 = 1, kF32 = 2 };             // 16-bit operand type / output type
+
+constexpr int kKB = 128;                                  // bytes of k per k-block
+
+// The saved pre-activations of the gated block: the upper 24 bits of the fp32
+// g and u (mantissa cut to 16 bits, relative error below 2^-15), as three
+// [T][I] planes of 16-bit words: g's upper half, u's upper half, and their
+// next 8 bits (g's in the low byte).  Rounding them to 16 bits instead would
+// cost the gradients a third rounding of the size of the operands' own.
+struct Saved {
+  uint16_t *g, *u, *lo;
+};
+struct SavedIn {
+  const uint16_t *g, *u, *lo;
+};
+
+struct Problem {
+  int64_t M, N;   // rows and columns of the output
+  int mt, nt;     // tiles
+  int tile0;      // first tile id
+  void* out;      // [M][N]
+};
+
+constexpr int kMaxProb = 3;
+struct Args {
+  CUtensorMap a[kMaxProb], b[kMaxProb];  // kGated: b[0] gate, b[1] up; segments or problems
+  Problem p[kMaxProb];
+  int nprob;       // products in the launch (each with a[i], b[i])
+  int nseg;        // k segments of one product (a[i], b[i] summed), 1 or 2; nprob 1 then
+  int kblocks;     // k-blocks of a segment
+  int tiles;
+  int type;        // 16-bit type of operands and outputs (Type), or kF32 outputs (kScaled)
+  uint32_t idesc;
+  const uint16_t* residual;        // kPlain: [M][N] or NULL
+  Saved saved;                     // kGated: planes to write (g NULL: none)
+  SavedIn in;                      // kDGate: planes to read
+  void* out2;                      // kDGate: du (p[0].out is dg)
+  const float *a_scale, *b_scale, *bias;  // kScaled
+  bool vec;                        // output rows are 16-byte aligned
+  uint64_t timeout_ns;
+};
+
+// ---------------------------------------------------------------- PTX wrappers
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
+                   : "memory");
+}
+__device__ __forceinline__ uint32_t map_to_rank(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+}
+__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+// TMA load into this CTA's shared memory that signals `bar` (a shared::cluster
+// address: the barrier of either CTA of the pair).
+__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap* map, int32_t c0,
+                                                 int32_t c1, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar)
+      : "memory");
+}
+template <int KIND>
+__device__ __forceinline__ void umma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                          uint32_t acc) {
+  if constexpr (KIND == kF16Kind)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+template <int KIND>
+__device__ __forceinline__ void umma_single(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                            uint32_t acc) {
+  if constexpr (KIND == kF16Kind)
+    umma_f16(d, a, b, idesc, acc);
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+// Arrives on the barrier at this offset in both CTAs of the pair.
+__device__ __forceinline__ void umma_commit_pair(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
+      " [%0], %1;" ::"r"(smem_u32(bar)),
+      "h"(static_cast<uint16_t>(3))
+      : "memory");
+}
+__device__ __forceinline__ void tmem_alloc_pair(uint32_t* slot, uint32_t ncols) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                   smem_u32(slot)),
+               "r"(ncols)
+               : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols)
+               : "memory");
+}
+
+// Instruction descriptor: accumulator type, operand types (16-bit: fp16 0,
+// bf16 1; 8-bit: signed 1), operand majors, tile size.
+__host__ __device__ constexpr uint32_t make_idesc(int kind, int type, bool a_mn, bool b_mn, int M,
+                                                  int N) {
+  const uint32_t d = kind == kI8Kind ? 2u : 1u;
+  const uint32_t ab = kind == kI8Kind ? 1u : (type == kF16 ? 0u : 1u);
+  return (d << 4) | (ab << 7) | (ab << 10) | (uint32_t(a_mn) << 15) | (uint32_t(b_mn) << 16) |
+         (uint32_t(N >> 3) << 17) | (uint32_t(M >> 4) << 24);
+}
+
+// Shared-memory operand descriptors with the 128-byte swizzle.  K-major: as
+// smem_desc_k128.  MN-major: 8-k groups 1024 bytes apart (stride offset),
+// 64-wide chunks 8192 bytes apart (leading offset).
+template <bool MN>
+__device__ __forceinline__ uint64_t operand_desc(uint32_t addr) {
+  if constexpr (!MN) return smem_desc_k128(addr);
+  return static_cast<uint64_t>((addr >> 4) & 0x3FFFu) | (uint64_t(8192 >> 4) << 16) |
+         (uint64_t(1024 >> 4) << 32) | (uint64_t(1) << 46) | (uint64_t(2) << 61);
+}
+// What one MMA's k (32 bytes) moves the descriptor's address by (in 16 bytes):
+// K-major along the swizzled row, MN-major by 16 k-rows of 128 bytes.
+template <bool MN>
+constexpr uint64_t kDescStep = MN ? (16 * 128) >> 4 : 32 >> 4;
+
+__device__ __forceinline__ uint32_t pack2(float lo, float hi, int type) {
+  if (type == kF16) {
+    __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<uint32_t*>(&v);
+  }
+  return pack_bf16x2(lo, hi);
+}
+__device__ __forceinline__ float unpack_lo(uint32_t v, int type) {
+  return type == kF16 ? f16_lo(v) : bf16_lo(v);
+}
+__device__ __forceinline__ float unpack_hi(uint32_t v, int type) {
+  return type == kF16 ? f16_hi(v) : bf16_hi(v);
+}
+__device__ __forceinline__ uint16_t pack1(float v, int type) {
+  return type == kF16 ? __half_as_ushort(__float2half_rn(v)) : __bfloat16_as_ushort(__float2bfloat16_rn(v));
+}
+__device__ __forceinline__ float unpack1(uint16_t v, int type) {
+  return type == kF16 ? __half2float(__ushort_as_half(v)) : __uint_as_float(uint32_t(v) << 16);
+}
+
+// silu and the two factors of its gradient.  For very negative g the
+// exponential overflows to infinity and sigma is 0, the limit; the products
+// with it stay finite.
+__device__ __forceinline__ float sigmoid(float g) { return __fdividef(1.0f, 1.0f + __expf(-g)); }
+__device__ __forceinline__ float silu(float g) { return __fdividef(g, 1.0f + __expf(-g)); }
+
+// ---------------------------------------------------------------- block stores
+
+constexpr int kStageRow = 80;                  // padded 64-byte row
+constexpr int kStageWarp = 32 * kStageRow;     // one warp's block
+
+// Stores a warp's block of 32 rows x 64 bytes (lane = row, its 16 words in pk)
+// at g0 (row 0, first column): through the warp's padded shared tile, so that
+// each row leaves as one 64-byte segment.  nrows rows and `ncols` columns
+// (elements of ES bytes) of it exist.  Rows that are not 16-byte aligned go
+// out element by element, lanes along the row.
+template <int ES>
+__device__ __forceinline__ void store_block(const uint32_t* pk, uint32_t stage, uint8_t* g0,
+                                            int64_t ld_bytes, int nrows, int64_t ncols, bool vec,
+                                            int lane) {
+  const uint32_t mine = stage + lane * kStageRow;
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+    st_shared_v4(mine + q * 16, pk[4 * q], pk[4 * q + 1], pk[4 * q + 2], pk[4 * q + 3]);
+  __syncwarp();
+  if (vec) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int row = i * 8 + (lane >> 2), ch = lane & 3;
+      const uint4 v = ld_shared_v4(stage + row * kStageRow + ch * 16);
+      if (row < nrows && (ch + 1) * (16 / ES) <= ncols)
+        st_global_v4(g0 + row * ld_bytes + ch * 16, v.x, v.y, v.z, v.w);
+    }
+  } else {
+    constexpr int PER = 64 / ES;               // elements of a row: 32 or 16
+    const int col = lane % PER;
+    for (int r = lane / PER; r < nrows; r += 32 / PER) {
+      if (col < ncols) {
+        if constexpr (ES == 2) {
+          uint16_t v;
+          asm volatile("ld.shared.b16 %0, [%1];" : "=h"(v) : "r"(stage + r * kStageRow + col * 2) : "memory");
+          *reinterpret_cast<uint16_t*>(g0 + r * ld_bytes + col * 2) = v;
+        } else {
+          uint32_t v;
+          asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(stage + r * kStageRow + col * 4) : "memory");
+          *reinterpret_cast<uint32_t*>(g0 + r * ld_bytes + col * 4) = v;
+        }
+      }
+    }
+  }
+  __syncwarp();
+}
+
+// 32 consecutive 16-bit words of a row (16-byte aligned, `ncols` of them
+// exist, a multiple of 8) as 16 packed pairs; what does not exist reads 0.
+__device__ __forceinline__ void load_row32(const uint16_t* p, bool row_ok, int64_t ncols,
+                                           uint32_t (&v)[16]) {
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    uint4 t = make_uint4(0u, 0u, 0u, 0u);
+    if (row_ok && (q + 1) * 8 <= ncols) t = *reinterpret_cast<const uint4*>(p + q * 8);
+    v[4 * q] = t.x; v[4 * q + 1] = t.y; v[4 * q + 2] = t.z; v[4 * q + 3] = t.w;
+  }
+}
+
+// ---------------------------------------------------------------- the pair kernel
+
+constexpr int kBM = 256;          // tile rows (128 per CTA)
+constexpr int kEpiWarps = 8;      // two per 32-lane quarter of tensor memory, a half of the columns each
+constexpr int kPairThreads = 32 * (kEpiWarps + 2);
+constexpr int kABytes = 128 * kKB;
+template <int BN>
+struct PairCfg {
+  static constexpr int B_BYTES = BN / 2 * kKB;
+  static constexpr int STAGE = kABytes + B_BYTES;
+  static constexpr int STAGES = BN == 256 ? 6 : 8;
+  static constexpr int SETS = 2;                          // accumulator sets of BN columns
+  static constexpr int TMEM = SETS * BN;
+  static constexpr int SMEM = STAGES * STAGE + kEpiWarps * kStageWarp + 1024 + 256;
+};
+struct PairTail {
+  uint64_t full[8], empty[8], tfull[2], tempty[2], drain;
+  uint32_t tmem_base;
+  int abort_flag;
+};
+static_assert(sizeof(PairTail) <= 256, "barriers fit their place");
+
+// Tile t of a launch: product q and tile coordinates.  Within a product the
+// tiles run over groups of 8 tile rows, row fastest, so that the clusters at
+// work at one time share rows of A and columns of B through L2.
+__device__ __forceinline__ void decode(const Args& g, int t, int& q, int& m, int& n) {
+  q = 0;
+  while (q + 1 < g.nprob && g.p[q + 1].tile0 <= t) ++q;
+  const int mt = g.p[q].mt, nt = g.p[q].nt;
+  t -= g.p[q].tile0;
+  const int per = 8 * nt, grp = t / per, rem = t - grp * per;
+  const int rows = min(8, mt - grp * 8);
+  n = rem / rows;
+  m = grp * 8 + (rem - n * rows);
+}
+
+template <int KIND, bool A_MN, bool B_MN, int EPI, int BN>
+__global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
+    pair_gemm_kernel(const __grid_constant__ Args g) {
+  using C = PairCfg<BN>;
+  constexpr int KE = KIND == kI8Kind ? 128 : 64;  // elements of a k-block
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint8_t* sEpi = smem + C::STAGES * C::STAGE;
+  PairTail* S = reinterpret_cast<PairTail*>(sEpi + kEpiWarps * kStageWarp);
+  volatile int* abort_flag = &S->abort_flag;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+  constexpr int kTmaWarp = kEpiWarps, kMmaWarp = kEpiWarps + 1;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::STAGES; ++s) {
+      mbar_init(&S->full[s], 1);
+      mbar_init(&S->empty[s], 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(&S->tfull[a], 1);
+      mbar_init(&S->tempty[a], 2 * kEpiWarps);
+    }
+    mbar_init(&S->drain, 1);
+    S->abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == kTmaWarp && lane == 0) {
+    for (int i = 0; i < kMaxProb; ++i) {
+      if (i < max(g.nprob, g.nseg)) tma_prefetch_desc(&g.a[i]);
+      if (i < max(g.nprob, g.nseg) + (EPI == kGated)) tma_prefetch_desc(&g.b[i]);
+    }
+  }
+  __syncwarp();
+  if (warp == kMmaWarp) tmem_alloc_pair(&S->tmem_base, C::TMEM);
+  tc_fence_before();
+  cluster_sync();  // barriers of both CTAs exist before either signals the other
+  tc_fence_after();
+  const uint32_t tmem = S->tmem_base;
+  griddep_wait();
+  griddep_launch_dependents();
+
+  const int cluster = blockIdx.x >> 1, nclusters = gridDim.x >> 1;
+  const int kbs = g.kblocks * g.nseg;
+
+  if (warp == kTmaWarp) {
+    if (lane == 0) {
+      int it = 0;
+      bool ok = true;
+      for (int t = cluster; ok && t < g.tiles; t += nclusters) {
+        int q, m, n;
+        decode(g, t, q, m, n);
+        const int m0 = m * kBM + static_cast<int>(rank) * 128;
+        // kGated: CTA 0 brings the gate columns, CTA 1 the up columns
+        const int n0 = EPI == kGated ? n * (BN / 2) : n * BN + static_cast<int>(rank) * (BN / 2);
+        for (int kb = 0; kb < kbs; ++kb, ++it) {
+          const int s = it % C::STAGES;
+          if (!mbar_wait(&S->empty[s], ((it / C::STAGES) & 1) ^ 1, abort_flag, g.timeout_ns, kSiteEmpty)) {
+            ok = false;
+            break;
+          }
+          const int seg = kb >= g.kblocks ? 1 : 0;
+          const int k0 = (kb - seg * g.kblocks) * KE;
+          const CUtensorMap* ma = &g.a[q + seg];
+          const CUtensorMap* mb = EPI == kGated ? &g.b[rank] : &g.b[q + seg];
+          const uint32_t sa = smem_u32(smem + s * C::STAGE), sb = sa + kABytes;
+          // both CTAs' bytes complete on the barrier of CTA 0, which issues the MMAs
+          if (rank == 0) mbar_arrive_expect_tx(&S->full[s], 2 * C::STAGE);
+          const uint32_t bar = map_to_rank(smem_u32(&S->full[s]), 0);
+          if constexpr (A_MN) {
+            tma_load_2d_pair(sa, ma, m0, k0, bar);
+            tma_load_2d_pair(sa + 8192, ma, m0 + 64, k0, bar);
+          } else {
+            tma_load_2d_pair(sa, ma, k0, m0, bar);
+          }
+          if constexpr (B_MN) {
+#pragma unroll
+            for (int c = 0; c < BN / 128; ++c) tma_load_2d_pair(sb + c * 8192, mb, n0 + c * 64, k0, bar);
+          } else {
+            tma_load_2d_pair(sb, mb, k0, n0, bar);
+          }
+        }
+      }
+      // After a wait that ran out, let the copies in flight land before either
+      // CTA can exit (otherwise the MMAs have consumed them all).  CTA 1's
+      // signal CTA 0's barriers, which it cannot wait on: it gives them 1 ms.
+      if (!ok && rank == 0)
+        for (int i = max(0, it - C::STAGES); i < it; ++i)
+          mbar_wait_drain(&S->full[i % C::STAGES], (i / C::STAGES) & 1, kSiteDrain);
+      if (!ok && rank == 1)
+        for (const uint64_t t0 = global_timer_ns(); global_timer_ns() - t0 < 1000000ull;) __nanosleep(1000);
+    }
+  } else if (warp == kMmaWarp) {
+    if (rank == 0 && lane == 0) {
+      int it = 0, n_tile = 0;
+      bool ok = true;
+      for (int t = cluster; ok && t < g.tiles; t += nclusters, ++n_tile) {
+        const int a = n_tile & 1;
+        if (!mbar_wait(&S->tempty[a], ((n_tile >> 1) & 1) ^ 1, abort_flag, g.timeout_ns, kSiteTmemEmpty)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t d = tmem + a * BN;
+        for (int kb = 0; kb < kbs; ++kb, ++it) {
+          const int s = it % C::STAGES;
+          if (!mbar_wait(&S->full[s], (it / C::STAGES) & 1, abort_flag, g.timeout_ns, kSiteFull)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t sa = smem_u32(smem + s * C::STAGE);
+          const uint64_t da = operand_desc<A_MN>(sa), db = operand_desc<B_MN>(sa + kABytes);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            umma_pair<KIND>(d, da + k * kDescStep<A_MN>, db + k * kDescStep<B_MN>, g.idesc, (kb | k) != 0);
+          umma_commit_pair(&S->empty[s]);
+        }
+        if (ok) umma_commit_pair(&S->tfull[a]);
+      }
+      if (!ok) {  // wait for the MMAs already issued
+        asm volatile(
+            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+                smem_u32(&S->drain))
+            : "memory");
+        mbar_wait_drain(&S->drain, 0, kSiteDrain);
+      }
+    }
+  } else {
+    // ---------------------------------------------- epilogue
+    const int quarter = warp & 3, half = warp >> 2;
+    const uint32_t stage = smem_u32(sEpi + warp * kStageWarp);
+    int n_tile = 0;
+    for (int t = cluster; t < g.tiles; t += nclusters, ++n_tile) {
+      int q, m, n;
+      decode(g, t, q, m, n);
+      const int a = n_tile & 1;
+      const Problem& P = g.p[q];
+      const int64_t row0 = int64_t(m) * kBM + rank * 128 + quarter * 32, row = row0 + lane;
+      const int nrows = static_cast<int>(min(int64_t(32), max(int64_t(0), P.M - row0)));
+      const bool row_ok = row < P.M;
+      if (!__all_sync(0xFFFFFFFFu, mbar_wait(&S->tfull[a], (n_tile >> 1) & 1, abort_flag,
+                                             g.timeout_ns, kSiteTmemFull)))
+        break;
+      tc_fence_after();
+      const uint32_t d = tmem + a * BN + (uint32_t(quarter * 32) << 16);
+      uint32_t x0[32], x1[32];
+      if constexpr (EPI == kGated) {
+        constexpr int W = BN / 4;  // output columns of this warp
+#pragma unroll 1
+        for (int c = 0; c < W; c += 32) {
+          const int lc = half * W + c;
+          tmem_ld_2x32(d + lc, d + BN / 2 + lc, x0, x1);
+          if (c + 32 >= W) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(map_to_rank(smem_u32(&S->tempty[a]), 0));
+          }
+          const int64_t col = int64_t(n) * (BN / 2) + lc, left = P.N - col;
+          if (left <= 0) continue;
+          const int64_t at = row0 * P.N + col;
+          uint32_t pk[16];
+          if (g.saved.g != nullptr) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) pk[i] = (x0[2 * i] >> 16) | (x0[2 * i + 1] & 0xFFFF0000u);
+            store_block<2>(pk, stage, reinterpret_cast<uint8_t*>(g.saved.g + at), P.N * 2, nrows, left, g.vec, lane);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) pk[i] = (x1[2 * i] >> 16) | (x1[2 * i + 1] & 0xFFFF0000u);
+            store_block<2>(pk, stage, reinterpret_cast<uint8_t*>(g.saved.u + at), P.N * 2, nrows, left, g.vec, lane);
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              pk[i] = ((x0[2 * i] >> 8) & 0xFFu) | (x1[2 * i] & 0xFF00u) |
+                      ((x0[2 * i + 1] << 8) & 0xFF0000u) | ((x1[2 * i + 1] << 16) & 0xFF000000u);
+            store_block<2>(pk, stage, reinterpret_cast<uint8_t*>(g.saved.lo + at), P.N * 2, nrows, left, g.vec, lane);
+          }
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            pk[i] = pack2(silu(__uint_as_float(x0[2 * i])) * __uint_as_float(x1[2 * i]),
+                          silu(__uint_as_float(x0[2 * i + 1])) * __uint_as_float(x1[2 * i + 1]), g.type);
+          store_block<2>(pk, stage, static_cast<uint8_t*>(P.out) + at * 2, P.N * 2, nrows, left, g.vec, lane);
+        }
+      } else {
+        constexpr int W = BN / 2;
+#pragma unroll 1
+        for (int c = 0; c < W; c += 64) {
+          const int lc = half * W + c;
+          tmem_ld_2x32(d + lc, d + lc + 32, x0, x1);
+          if (c + 64 >= W) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(map_to_rank(smem_u32(&S->tempty[a]), 0));
+          }
+#pragma unroll
+          for (int hh = 0; hh < 2; ++hh) {
+            uint32_t(&x)[32] = hh ? x1 : x0;
+            const int64_t col = int64_t(n) * BN + lc + hh * 32, left = P.N - col;
+            if (left <= 0) continue;
+            const int64_t at = row0 * P.N + col;
+            uint32_t pk[16];
+            if constexpr (EPI == kPlain) {
+              if (g.residual != nullptr) {
+                uint32_t r[16];
+                load_row32(g.residual + at + lane * P.N, row_ok, left, r);
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                  pk[i] = pack2(__uint_as_float(x[2 * i]) + unpack_lo(r[i], g.type),
+                                __uint_as_float(x[2 * i + 1]) + unpack_hi(r[i], g.type), g.type);
+              } else {
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                  pk[i] = pack2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]), g.type);
+              }
+              store_block<2>(pk, stage, static_cast<uint8_t*>(P.out) + at * 2, P.N * 2, nrows, left, g.vec, lane);
+            } else if constexpr (EPI == kDGate) {
+              uint32_t gh[16], uh[16], lo[16], pg[16];
+              load_row32(g.in.g + at + lane * P.N, row_ok, left, gh);
+              load_row32(g.in.u + at + lane * P.N, row_ok, left, uh);
+              load_row32(g.in.lo + at + lane * P.N, row_ok, left, lo);
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                float dg[2], du[2];
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                  const uint32_t l = lo[i] >> (16 * j);
+                  const float gg = __uint_as_float((j ? gh[i] & 0xFFFF0000u : gh[i] << 16) | ((l & 0xFFu) << 8));
+                  const float uu = __uint_as_float((j ? uh[i] & 0xFFFF0000u : uh[i] << 16) | (l & 0xFF00u));
+                  const float dh = __uint_as_float(x[2 * i + j]);
+                  const float sg = sigmoid(gg), act = silu(gg);
+                  du[j] = dh * act;
+                  dg[j] = dh * uu * (sg + act * (1.f - sg));
+                }
+                pg[i] = pack2(dg[0], dg[1], g.type);
+                pk[i] = pack2(du[0], du[1], g.type);
+              }
+              store_block<2>(pg, stage, static_cast<uint8_t*>(P.out) + at * 2, P.N * 2, nrows, left, g.vec, lane);
+              store_block<2>(pk, stage, static_cast<uint8_t*>(g.out2) + at * 2, P.N * 2, nrows, left, g.vec, lane);
+            } else {
+              const float sa = row_ok ? g.a_scale[row] : 0.f;
+              float y[32];
+#pragma unroll
+              for (int i = 0; i < 32; ++i) {
+                const bool in = i < left;
+                const float sb = in ? g.b_scale[col + i] : 0.f;
+                y[i] = static_cast<float>(static_cast<int>(x[i])) * sa * sb;
+                if (g.bias != nullptr && in) y[i] += g.bias[col + i];
+              }
+              if (g.type == kF32) {
+#pragma unroll
+                for (int f = 0; f < 2; ++f) {
+#pragma unroll
+                  for (int i = 0; i < 16; ++i) pk[i] = __float_as_uint(y[f * 16 + i]);
+                  if (left > f * 16)
+                    store_block<4>(pk, stage, static_cast<uint8_t*>(P.out) + (at + f * 16) * 4, P.N * 4, nrows,
+                                   left - f * 16, g.vec, lane);
+                }
+              } else {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) pk[i] = pack2(y[2 * i], y[2 * i + 1], g.type);
+                store_block<2>(pk, stage, static_cast<uint8_t*>(P.out) + at * 2, P.N * 2, nrows, left, g.vec, lane);
+              }
+            }
+          }
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncwarp();
+  cluster_sync();  // neither CTA leaves while the other may still signal it
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, C::TMEM);
+  }
+}
+
+}  // namespace dense
+}  // namespace moe

@@ -1,0 +1,563 @@
+// dense_host.cuh -- host side of the norm (norm.cuh) and of the dense products
+// (dense.cuh, dense_small.cuh): argument checks, tensor maps, choice of the
+// kernel, launches, and the pre-norm layer.  A part of moe.cu, whose helpers it
+// uses.
+#pragma once
+
+namespace {
+
+// ---- norm ------------------------------------------------------------------------
+bool type16(int t) { return t == MOE_TYPE_BF16 || t == MOE_TYPE_F16; }
+
+// Block shape of a row of H: threads and packs per thread (a power of two).
+struct RowShape {
+  int threads, nv;
+};
+RowShape row_shape(int64_t nvec) {
+  int nv = 1;
+  while (nv < 4 && nvec > 256 * nv) nv *= 2;  // up to 256 threads as long as 4 packs do
+  while (nvec > 1024 * int64_t(nv)) nv *= 2;
+  const int64_t per = (nvec + nv - 1) / nv;
+  return {static_cast<int>((per + 31) / 32 * 32), nv};
+}
+
+template <typename E, int VEC, int NV>
+int launch_norm_fmt(int fmt, const RowShape& rs, int64_t T, const void* x, const void* res, const void* w,
+                    float eps, int H, int group, void* s_out, void* out, float* scales, cudaStream_t s) {
+  auto k = fmt == norm::kSame   ? norm::add_rmsnorm_kernel<E, VEC, NV, norm::kSame>
+           : fmt == norm::kInt8 ? norm::add_rmsnorm_kernel<E, VEC, NV, norm::kInt8>
+                                : norm::add_rmsnorm_kernel<E, VEC, NV, norm::kE4m3>;
+  return launch_pdl("add_rmsnorm_kernel launch", k, dim3(static_cast<unsigned>(T)), dim3(rs.threads), 0, s,
+                    static_cast<const E*>(x), static_cast<const E*>(res), static_cast<const E*>(w), eps, H,
+                    group, static_cast<E*>(s_out), out, scales);
+}
+template <typename E, int VEC>
+int launch_norm(int fmt, int64_t T, const void* x, const void* res, const void* w, float eps, int H,
+                int group, void* s_out, void* out, float* scales, cudaStream_t s) {
+  const RowShape rs = row_shape(H / VEC);
+  switch (rs.nv) {
+    case 1: return launch_norm_fmt<E, VEC, 1>(fmt, rs, T, x, res, w, eps, H, group, s_out, out, scales, s);
+    case 2: return launch_norm_fmt<E, VEC, 2>(fmt, rs, T, x, res, w, eps, H, group, s_out, out, scales, s);
+    case 4: return launch_norm_fmt<E, VEC, 4>(fmt, rs, T, x, res, w, eps, H, group, s_out, out, scales, s);
+    default: break;
+  }
+  if constexpr (VEC == 1) {
+    if (rs.nv == 8) return launch_norm_fmt<E, 1, 8>(fmt, rs, T, x, res, w, eps, H, group, s_out, out, scales, s);
+    if (rs.nv == 16) return launch_norm_fmt<E, 1, 16>(fmt, rs, T, x, res, w, eps, H, group, s_out, out, scales, s);
+    if (rs.nv == 32) return launch_norm_fmt<E, 1, 32>(fmt, rs, T, x, res, w, eps, H, group, s_out, out, scales, s);
+  }
+  return fail(MOE_ERR_INVALID_ARG, "H=%d", H);
+}
+
+int do_add_rmsnorm(int type, int fmt, int64_t T, const void* x, const void* res, const void* w, float eps,
+                   int H, int group, void* s_out, void* out, float* scales, cudaStream_t s) {
+  // 16-byte accesses need every row to start on 16 bytes (8-bit rows: 8)
+  if (type == MOE_TYPE_BF16)
+    return H % 8 == 0 ? launch_norm<__nv_bfloat16, 8>(fmt, T, x, res, w, eps, H, group, s_out, out, scales, s)
+                      : launch_norm<__nv_bfloat16, 1>(fmt, T, x, res, w, eps, H, group, s_out, out, scales, s);
+  return H % 8 == 0 ? launch_norm<__half, 8>(fmt, T, x, res, w, eps, H, group, s_out, out, scales, s)
+                    : launch_norm<__half, 1>(fmt, T, x, res, w, eps, H, group, s_out, out, scales, s);
+}
+
+template <typename E, int VEC>
+int launch_norm_bwd(int64_t T, const void* dy, const void* sv, const void* w, float eps, int H,
+                    const void* dstream, void* dx, float* parts, int blocks, cudaStream_t s) {
+  const RowShape rs = row_shape(H / VEC);
+  auto go = [&](auto k) {
+    return launch_pdl("rmsnorm_backward_kernel launch", k, dim3(blocks), dim3(rs.threads), 0, s,
+                      static_cast<const E*>(dy), static_cast<const E*>(sv), static_cast<const E*>(w), eps, T, H,
+                      static_cast<const E*>(dstream), static_cast<E*>(dx), parts);
+  };
+  switch (rs.nv) {
+    case 1: return go(norm::rmsnorm_backward_kernel<E, VEC, 1>);
+    case 2: return go(norm::rmsnorm_backward_kernel<E, VEC, 2>);
+    case 4: return go(norm::rmsnorm_backward_kernel<E, VEC, 4>);
+    default: break;
+  }
+  if constexpr (VEC == 1) {
+    if (rs.nv == 8) return go(norm::rmsnorm_backward_kernel<E, 1, 8>);
+    if (rs.nv == 16) return go(norm::rmsnorm_backward_kernel<E, 1, 16>);
+    if (rs.nv == 32) return go(norm::rmsnorm_backward_kernel<E, 1, 32>);
+  }
+  return fail(MOE_ERR_INVALID_ARG, "H=%d", H);
+}
+
+int norm_parts(int64_t T) { return static_cast<int>(std::min<int64_t>(T, norm::kMaxParts)); }
+
+int check_norm_H(int64_t H) {
+  REQUIRE(H >= 1 && H <= norm::kMaxH, "H=%lld outside [1, %d]", static_cast<long long>(H), norm::kMaxH);
+  return MOE_OK;
+}
+
+// ---- dense products -----------------------------------------------------------------
+constexpr int64_t kMaxDim = 65536;        // widths of the gated block
+constexpr int64_t kMaxInt8N = 1 << 20;    // channels of the int8 product
+constexpr int64_t kMaxInt8K = 131056;     // K * 128 * 128 < 2^31: the int32 sums cannot overflow
+constexpr int64_t kSmallMaxT = 128;       // tokens up to which the weights are the MMA's rows
+
+// Row-major matrix of `rows` rows of `cols` elements (1 or 2 bytes), boxes of
+// 128 bytes x box_rows, 128-byte swizzle; outside the matrix reads zero.
+int make_map(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int elem, int box_rows) {
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols) * elem};
+  const cuuint32_t box[2] = {static_cast<cuuint32_t>(128 / elem), static_cast<cuuint32_t>(box_rows)};
+  const cuuint32_t estr[2] = {1, 1};
+  const CUresult r = g_encode(m, elem == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 2,
+                              const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(MOE_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", int(r));
+  return MOE_OK;
+}
+
+// An operand: rows x cols as it lies in memory; mn: its m (or n) runs along a
+// row (else k does).
+struct Operand {
+  const void* p;
+  int64_t rows, cols;
+  bool mn;
+  int64_t k() const { return mn ? rows : cols; }
+  int64_t outer() const { return mn ? cols : rows; }
+};
+
+template <int KIND, bool A_MN, bool B_MN, int EPI>
+auto pair_kernel(int bn) {
+  return bn == 256 ? dense::pair_gemm_kernel<KIND, A_MN, B_MN, EPI, 256>
+                   : dense::pair_gemm_kernel<KIND, A_MN, B_MN, EPI, 128>;
+}
+
+// What one launch computes, before a kernel is chosen for it.
+struct Product {
+  Operand a[dense::kMaxProb], b[dense::kMaxProb];
+  void* out[dense::kMaxProb];
+  int nprob = 1, nseg = 1;
+  int type = dense::kBF16;  // operand type, or kF32 outputs of int8
+  const void* residual = nullptr;
+  void* saved = nullptr;     // three planes of M*N words (kGated: out, kDGate: in)
+  void* out2 = nullptr;
+  const float *a_scale = nullptr, *b_scale = nullptr, *bias = nullptr;
+};
+
+template <typename A>
+void common_args(A* g, const Product& p, int64_t M, int64_t N) {
+  g->type = p.type;
+  g->residual = static_cast<const uint16_t*>(p.residual);
+  uint16_t* s = static_cast<uint16_t*>(p.saved);
+  if (s != nullptr) {
+    g->saved = {s, s + M * N, s + 2 * M * N};
+    g->in = {s, s + M * N, s + 2 * M * N};
+  }
+  g->out2 = p.out2;
+  g->a_scale = p.a_scale;
+  g->b_scale = p.b_scale;
+  g->bias = p.bias;
+  g->timeout_ns = g_timeout_ns.load();
+}
+
+int64_t div_up(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+template <int KIND, bool A_MN, bool B_MN, int EPI>
+int launch_pair(const Product& p, int sms, cudaStream_t s) {
+  const int elem = KIND == dense::kI8Kind ? 1 : 2, ke = 128 / elem;
+  auto tiles_of = [&](int bn) {
+    int64_t n = 0;
+    for (int i = 0; i < p.nprob; ++i)
+      n += div_up(p.a[i].outer(), dense::kBM) *
+           div_up(p.b[i].outer(), EPI == dense::kGated ? bn / 2 : bn);
+    return n;
+  };
+  // 256-column tiles feed the tensor cores best; with fewer of them than
+  // clusters, 128-column ones put more SMs to work
+  const int bn = tiles_of(256) >= sms / 2 ? 256 : 128;
+  dense::Args g{};
+  g.nprob = p.nprob;
+  g.nseg = p.nseg;
+  g.kblocks = static_cast<int>(div_up(p.a[0].k(), ke));
+  int64_t tiles = 0;
+  const int nmaps = p.nprob > 1 ? p.nprob : p.nseg;
+  for (int i = 0; i < nmaps; ++i) {
+    int rc = make_map(&g.a[i], p.a[i].p, p.a[i].rows, p.a[i].cols, elem, A_MN ? 64 : 128);
+    if (!rc) rc = make_map(&g.b[i], p.b[i].p, p.b[i].rows, p.b[i].cols, elem, B_MN ? 64 : bn / 2);
+    if (rc) return rc;
+  }
+  if (EPI == dense::kGated) {  // b[1]: the up weights
+    int rc = make_map(&g.b[1], p.b[1].p, p.b[1].rows, p.b[1].cols, elem, 64);
+    if (rc) return rc;
+  }
+  g.vec = true;
+  for (int i = 0; i < p.nprob; ++i) {
+    dense::Problem& q = g.p[i];
+    q.M = p.a[i].outer();
+    q.N = p.b[i].outer();
+    q.mt = static_cast<int>(div_up(q.M, dense::kBM));
+    q.nt = static_cast<int>(div_up(q.N, EPI == dense::kGated ? bn / 2 : bn));
+    q.tile0 = static_cast<int>(tiles);
+    q.out = p.out[i];
+    tiles += int64_t(q.mt) * q.nt;
+    g.vec = g.vec && (q.N * (p.type == dense::kF32 ? 4 : 2)) % 16 == 0;
+  }
+  g.tiles = static_cast<int>(tiles);
+  common_args(&g, p, g.p[0].M, g.p[0].N);
+  g.idesc = dense::make_idesc(KIND, p.type, A_MN, B_MN, dense::kBM, bn);
+  const unsigned grid = 2 * static_cast<unsigned>(std::min<int64_t>(tiles, sms / 2));
+  const size_t smem = bn == 256 ? dense::PairCfg<256>::SMEM : dense::PairCfg<128>::SMEM;
+  return launch_pdl("pair_gemm_kernel launch", pair_kernel<KIND, A_MN, B_MN, EPI>(bn), dim3(grid),
+                    dim3(dense::kPairThreads), smem, s, g);
+}
+
+template <int KIND, bool W_MN, int EPI, int NT>
+int launch_small_nt(const Product& p, int sms, cudaStream_t s) {
+  const int elem = KIND == dense::kI8Kind ? 1 : 2, ke = 128 / elem;
+  dense::SmallArgs g{};
+  g.T = p.a[0].outer();
+  g.N = p.b[0].outer();
+  g.nseg = p.nseg;
+  g.kblocks = static_cast<int>(div_up(p.a[0].k(), ke));
+  g.wt = static_cast<int>(div_up(g.N, EPI == dense::kGated ? 64 : dense::kSmallRows));
+  const int64_t tiles = g.wt * div_up(g.T, NT);
+  for (int i = 0; i < p.nseg; ++i) {
+    int rc = make_map(&g.x[i], p.a[i].p, p.a[i].rows, p.a[i].cols, elem, NT);
+    if (!rc) rc = make_map(&g.w[i], p.b[i].p, p.b[i].rows, p.b[i].cols, elem, W_MN ? 64 : dense::kSmallRows);
+    if (rc) return rc;
+  }
+  if (EPI == dense::kGated) {
+    int rc = make_map(&g.w[1], p.b[1].p, p.b[1].rows, p.b[1].cols, elem, 64);
+    if (rc) return rc;
+  }
+  // split k over the cluster until the CTAs fill the SMs twice, as long as
+  // each keeps 2 k-blocks
+  g.split = 1;
+  while (g.split < 8 && tiles * g.split * 2 <= 2 * sms && g.kblocks * g.nseg >= g.split * 4) g.split *= 2;
+  g.out = p.out[0];
+  common_args(&g, p, g.T, g.N);
+  g.idesc = dense::make_idesc(KIND, p.type, W_MN, false, dense::kSmallRows, NT);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(tiles * g.split));
+  cfg.blockDim = dim3(dense::kSmallThreads);
+  cfg.dynamicSmemBytes = dense::SmallCfg<NT>::SMEM;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(g.split);
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, dense::small_gemm_kernel<KIND, W_MN, EPI, NT>, g);
+  if (e != cudaSuccess) return cuda_fail(e, "small_gemm_kernel launch");
+  return MOE_OK;
+}
+
+template <int KIND, bool B_MN, int EPI>
+int launch_product(const Product& p, int sms, cudaStream_t s) {
+  const int64_t T = p.a[0].outer();
+  if (T <= 16) return launch_small_nt<KIND, B_MN, EPI, 16>(p, sms, s);
+  if (T <= 32) return launch_small_nt<KIND, B_MN, EPI, 32>(p, sms, s);
+  if (T <= 64) return launch_small_nt<KIND, B_MN, EPI, 64>(p, sms, s);
+  if (T <= kSmallMaxT) return launch_small_nt<KIND, B_MN, EPI, 128>(p, sms, s);
+  return launch_pair<KIND, false, B_MN, EPI>(p, sms, s);
+}
+
+template <int KIND, bool A_MN, bool B_MN, int EPI>
+cudaError_t pair_attr() {
+  cudaError_t e = cudaFuncSetAttribute(dense::pair_gemm_kernel<KIND, A_MN, B_MN, EPI, 256>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, dense::PairCfg<256>::SMEM);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(dense::pair_gemm_kernel<KIND, A_MN, B_MN, EPI, 128>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, dense::PairCfg<128>::SMEM);
+  return e;
+}
+template <int KIND, bool W_MN, int EPI, int NT>
+cudaError_t small_attr_nt() {
+  return cudaFuncSetAttribute(dense::small_gemm_kernel<KIND, W_MN, EPI, NT>,
+                              cudaFuncAttributeMaxDynamicSharedMemorySize, dense::SmallCfg<NT>::SMEM);
+}
+template <int KIND, bool W_MN, int EPI>
+cudaError_t small_attr() {
+  cudaError_t e = small_attr_nt<KIND, W_MN, EPI, 16>();
+  if (e == cudaSuccess) e = small_attr_nt<KIND, W_MN, EPI, 32>();
+  if (e == cudaSuccess) e = small_attr_nt<KIND, W_MN, EPI, 64>();
+  if (e == cudaSuccess) e = small_attr_nt<KIND, W_MN, EPI, 128>();
+  return e;
+}
+cudaError_t dense_attributes() {
+  using namespace dense;
+  cudaError_t e = pair_attr<kF16Kind, false, true, kGated>();
+  if (e == cudaSuccess) e = pair_attr<kF16Kind, false, true, kPlain>();
+  if (e == cudaSuccess) e = pair_attr<kF16Kind, false, false, kPlain>();
+  if (e == cudaSuccess) e = pair_attr<kF16Kind, false, false, kDGate>();
+  if (e == cudaSuccess) e = pair_attr<kF16Kind, true, true, kPlain>();
+  if (e == cudaSuccess) e = pair_attr<kI8Kind, false, false, kScaled>();
+  if (e == cudaSuccess) e = small_attr<kF16Kind, true, kGated>();
+  if (e == cudaSuccess) e = small_attr<kF16Kind, true, kPlain>();
+  if (e == cudaSuccess) e = small_attr<kF16Kind, false, kPlain>();
+  if (e == cudaSuccess) e = small_attr<kF16Kind, false, kDGate>();
+  if (e == cudaSuccess) e = small_attr<kI8Kind, false, kScaled>();
+  return e;
+}
+
+int check_ffn(int64_t T, int64_t H, int64_t I, int dtype) {
+  int rc = check_T(T);
+  if (rc) return rc;
+  REQUIRE(H >= 8 && H <= kMaxDim && H % 8 == 0 && I >= 8 && I <= kMaxDim && I % 8 == 0,
+          "H=%lld and I=%lld must be multiples of 8 in [8, %lld]", static_cast<long long>(H),
+          static_cast<long long>(I), static_cast<long long>(kMaxDim));
+  REQUIRE(type16(dtype), "dtype=%d: bf16 or fp16", dtype);
+  return MOE_OK;
+}
+
+}  // namespace
+
+// The public type codes are the kernels' own.
+static_assert(int(MOE_TYPE_BF16) == dense::kBF16 && int(MOE_TYPE_F16) == dense::kF16 &&
+                  int(MOE_TYPE_F32) == dense::kF32,
+              "types");
+static_assert(int(MOE_FORMAT_SAME) == norm::kSame && int(MOE_FORMAT_INT8) == norm::kInt8 &&
+                  int(MOE_FORMAT_E4M3) == norm::kE4m3,
+              "formats");
+
+extern "C" {
+
+int moe_add_rmsnorm(const void* x, const void* residual, const void* weight, float eps, int64_t T,
+                    int64_t H, int dtype, void* stream_out, int format, int group, void* out,
+                    float* scales, moe_stream_t stream) {
+  int rc = check_T(T);
+  if (!rc) rc = check_norm_H(H);
+  if (rc) return rc;
+  REQUIRE(type16(dtype), "dtype=%d: bf16 or fp16", dtype);
+  REQUIRE(format >= MOE_FORMAT_SAME && format <= MOE_FORMAT_E4M3, "format=%d", format);
+  REQUIRE(group == 0 || (group == norm::kGroup && format != MOE_FORMAT_SAME),
+          "group=%d: 0, or %d with an 8-bit format", group, norm::kGroup);
+  REQUIRE(eps >= 0.f && eps < INFINITY, "eps must be finite and not negative");
+  if (T == 0) return MOE_OK;
+  REQUIRE(x && out && (!residual || stream_out) && (format == MOE_FORMAT_SAME || scales), "null pointer");
+  REQUIRE(aligned(x, 16) && aligned(out, 16) && aligned(residual, 16) && aligned(weight, 16) &&
+              aligned(stream_out, 16) && aligned(scales, 16),
+          "pointers must be 16-byte aligned");
+  rc = device_setup(nullptr, nullptr);
+  if (rc) return rc;
+  return do_add_rmsnorm(dtype, format, T, x, residual, weight, eps, static_cast<int>(H), group, stream_out, out,
+                        scales, reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t moe_add_rmsnorm_backward_workspace_bytes(int64_t T, int64_t H) {
+  if (T < 0 || T > kMaxTokens || H < 1 || H > norm::kMaxH) return 0;
+  return static_cast<size_t>(norm_parts(T)) * static_cast<size_t>(H) * sizeof(float);
+}
+
+int moe_add_rmsnorm_backward(const void* dy, const void* s, const void* weight, float eps, int64_t T,
+                             int64_t H, int dtype, const void* dstream, void* dx, float* dweight,
+                             void* workspace, size_t workspace_bytes, moe_stream_t stream) {
+  int rc = check_T(T);
+  if (!rc) rc = check_norm_H(H);
+  if (rc) return rc;
+  REQUIRE(type16(dtype), "dtype=%d: bf16 or fp16", dtype);
+  REQUIRE(eps >= 0.f && eps < INFINITY, "eps must be finite and not negative");
+  REQUIRE(aligned(dy, 16) && aligned(s, 16) && aligned(weight, 16) && aligned(dstream, 16) && aligned(dx, 16) &&
+              aligned(dweight, 16) && aligned(workspace, 16),
+          "pointers must be 16-byte aligned");
+  REQUIRE(T == 0 || (dy && s && dx), "null pointer");
+  const size_t need = dweight ? moe_add_rmsnorm_backward_workspace_bytes(T, H) : 0;
+  if (need && (workspace == nullptr || workspace_bytes < need))
+    return fail(MOE_ERR_WORKSPACE, "moe_add_rmsnorm_backward workspace needs %zu bytes, got %zu", need,
+                workspace ? workspace_bytes : size_t(0));
+  if (T == 0 && !dweight) return MOE_OK;
+  rc = device_setup(nullptr, nullptr);
+  if (rc) return rc;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (T == 0) {  // the gradient of no tokens
+    MOE_CUDA(cudaMemsetAsync(dweight, 0, static_cast<size_t>(H) * sizeof(float), st), "cudaMemsetAsync");
+    return MOE_OK;
+  }
+  float* parts = dweight ? static_cast<float*>(workspace) : nullptr;
+  const int blocks = norm_parts(T), h = static_cast<int>(H);
+  if (dtype == MOE_TYPE_BF16)
+    rc = h % 8 == 0 ? launch_norm_bwd<__nv_bfloat16, 8>(T, dy, s, weight, eps, h, dstream, dx, parts, blocks, st)
+                    : launch_norm_bwd<__nv_bfloat16, 1>(T, dy, s, weight, eps, h, dstream, dx, parts, blocks, st);
+  else
+    rc = h % 8 == 0 ? launch_norm_bwd<__half, 8>(T, dy, s, weight, eps, h, dstream, dx, parts, blocks, st)
+                    : launch_norm_bwd<__half, 1>(T, dy, s, weight, eps, h, dstream, dx, parts, blocks, st);
+  if (rc || !dweight) return rc;
+  return launch_pdl("rmsnorm_dw_kernel launch", norm::rmsnorm_dw_kernel, dim3((h + 31) / 32), dim3(256), 0, st,
+                    static_cast<const float*>(parts), blocks, h, dweight);
+}
+
+int moe_int8_matmul(const int8_t* a, const float* a_scale, const int8_t* b, const float* b_scale,
+                    const float* bias, int64_t T, int64_t N, int64_t K, int out_dtype, void* out,
+                    moe_stream_t stream) {
+  int rc = check_T(T);
+  if (rc) return rc;
+  REQUIRE(N >= 1 && N <= kMaxInt8N, "N=%lld outside [1, %lld]", static_cast<long long>(N),
+          static_cast<long long>(kMaxInt8N));
+  REQUIRE(K >= 16 && K <= kMaxInt8K && K % 16 == 0, "K=%lld must be a multiple of 16 in [16, %lld]",
+          static_cast<long long>(K), static_cast<long long>(kMaxInt8K));
+  REQUIRE(type16(out_dtype) || out_dtype == MOE_TYPE_F32, "out_dtype=%d: bf16, fp16 or fp32", out_dtype);
+  if (T == 0) return MOE_OK;
+  REQUIRE(a && a_scale && b && b_scale && out, "null pointer");
+  REQUIRE(aligned(a, 16) && aligned(a_scale, 16) && aligned(b, 16) && aligned(b_scale, 16) && aligned(bias, 16) &&
+              aligned(out, 16),
+          "pointers must be 16-byte aligned");
+  int sms = 0;
+  rc = device_setup(nullptr, &sms);
+  if (rc) return rc;
+  Product p{};
+  p.a[0] = {a, T, K, false};
+  p.b[0] = {b, N, K, false};
+  p.out[0] = out;
+  p.type = out_dtype;
+  p.a_scale = a_scale;
+  p.b_scale = b_scale;
+  p.bias = bias;
+  return launch_product<dense::kI8Kind, false, dense::kScaled>(p, sms, reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t moe_gated_ffn_saved_bytes(int64_t T, int64_t I) {
+  if (T < 0 || T > kMaxTokens || I < 0 || I > kMaxDim) return 0;
+  return static_cast<size_t>(T) * static_cast<size_t>(I) * 6;
+}
+
+int moe_gated_ffn(const void* x, const void* w_gate, const void* w_up, const void* w_down, int64_t T,
+                  int64_t H, int64_t I, int dtype, const void* residual, void* h, void* saved, void* y,
+                  moe_stream_t stream) {
+  int rc = check_ffn(T, H, I, dtype);
+  if (rc) return rc;
+  if (T == 0) return MOE_OK;
+  REQUIRE(x && w_gate && w_up && w_down && h && y, "null pointer");
+  REQUIRE(aligned(x, 16) && aligned(w_gate, 16) && aligned(w_up, 16) && aligned(w_down, 16) && aligned(h, 16) &&
+              aligned(saved, 16) && aligned(y, 16) && aligned(residual, 16),
+          "pointers must be 16-byte aligned");
+  int sms = 0;
+  rc = device_setup(nullptr, &sms);
+  if (rc) return rc;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  Product up{};
+  up.a[0] = {x, T, H, false};
+  up.b[0] = {w_gate, H, I, true};
+  up.b[1] = {w_up, H, I, true};
+  up.out[0] = h;
+  up.type = dtype;
+  up.saved = saved;
+  rc = launch_product<dense::kF16Kind, true, dense::kGated>(up, sms, s);
+  if (rc) return rc;
+  Product down{};
+  down.a[0] = {h, T, I, false};
+  down.b[0] = {w_down, I, H, true};
+  down.out[0] = y;
+  down.type = dtype;
+  down.residual = residual;
+  return launch_product<dense::kF16Kind, true, dense::kPlain>(down, sms, s);
+}
+
+size_t moe_gated_ffn_backward_workspace_bytes(int64_t T, int64_t I) {
+  if (T < 0 || T > kMaxTokens || I < 0 || I > kMaxDim) return 0;
+  return static_cast<size_t>(T) * static_cast<size_t>(I) * 4;
+}
+
+int moe_gated_ffn_backward(const void* dy, const void* x, const void* w_gate, const void* w_up,
+                           const void* w_down, const void* h, const void* saved, int64_t T, int64_t H,
+                           int64_t I, int dtype, void* dx, void* dw_gate, void* dw_up, void* dw_down,
+                           void* workspace, size_t workspace_bytes, moe_stream_t stream) {
+  int rc = check_ffn(T, H, I, dtype);
+  if (rc) return rc;
+  REQUIRE(aligned(dy, 16) && aligned(x, 16) && aligned(w_gate, 16) && aligned(w_up, 16) && aligned(w_down, 16) &&
+              aligned(h, 16) && aligned(saved, 16) && aligned(dx, 16) && aligned(dw_gate, 16) && aligned(dw_up, 16) &&
+              aligned(dw_down, 16) && aligned(workspace, 16),
+          "pointers must be 16-byte aligned");
+  void* dw[3] = {dw_gate, dw_up, dw_down};
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  int sms = 0;
+  if (T == 0) {  // the gradients of no tokens
+    rc = device_setup(nullptr, &sms);
+    if (rc) return rc;
+    for (void* d : dw)
+      if (d) MOE_CUDA(cudaMemsetAsync(d, 0, static_cast<size_t>(H) * static_cast<size_t>(I) * 2, s), "cudaMemsetAsync");
+    return MOE_OK;
+  }
+  const bool need_d = dx || dw_gate || dw_up;  // dg and du
+  REQUIRE(dy && (!need_d || (w_down && saved)) && (!dx || (w_gate && w_up)) && (!(dw_gate || dw_up) || x) &&
+              (!dw_down || h),
+          "null pointer");
+  const size_t need = need_d ? moe_gated_ffn_backward_workspace_bytes(T, I) : 0;
+  if (need && (workspace == nullptr || workspace_bytes < need))
+    return fail(MOE_ERR_WORKSPACE, "moe_gated_ffn_backward workspace needs %zu bytes, got %zu", need,
+                workspace ? workspace_bytes : size_t(0));
+  rc = device_setup(nullptr, &sms);
+  if (rc) return rc;
+  char* dg = static_cast<char*>(workspace);
+  char* du = dg + static_cast<size_t>(T) * static_cast<size_t>(I) * 2;
+  if (need_d) {
+    Product p{};
+    p.a[0] = {dy, T, H, false};
+    p.b[0] = {w_down, I, H, false};
+    p.out[0] = dg;
+    p.out2 = du;
+    p.type = dtype;
+    p.saved = const_cast<void*>(saved);
+    rc = launch_product<dense::kF16Kind, false, dense::kDGate>(p, sms, s);
+    if (rc) return rc;
+  }
+  if (dx) {
+    Product p{};
+    p.a[0] = {dg, T, I, false};
+    p.a[1] = {du, T, I, false};
+    p.b[0] = {w_gate, H, I, false};
+    p.b[1] = {w_up, H, I, false};
+    p.nseg = 2;
+    p.out[0] = dx;
+    p.type = dtype;
+    rc = launch_product<dense::kF16Kind, false, dense::kPlain>(p, sms, s);
+    if (rc) return rc;
+  }
+  // the weights' gradients asked for, in one launch
+  Product p{};
+  p.nprob = 0;
+  p.type = dtype;
+  for (int i = 0; i < 3; ++i) {
+    if (!dw[i]) continue;
+    const int j = p.nprob++;
+    if (i < 2) {
+      p.a[j] = {x, T, H, true};
+      p.b[j] = {i == 0 ? dg : du, T, I, true};
+    } else {
+      p.a[j] = {h, T, I, true};
+      p.b[j] = {dy, T, H, true};
+    }
+    p.out[j] = dw[i];
+  }
+  if (p.nprob == 0) return MOE_OK;
+  return launch_pair<dense::kF16Kind, true, true, dense::kPlain>(p, sms, s);
+}
+
+// ---- the pre-norm layer ------------------------------------------------------------
+size_t moe_layer_normed_workspace_bytes(int64_t T) {
+  if (T < 0 || T > kMaxTokens) return 0;
+  return align_up(layer_ws(T, false, 0).total, 1024) + align_up(static_cast<size_t>(T) * kH * 2, 1024);
+}
+
+int moe_layer_normed(const moe_bf16* x, const moe_bf16* residual, const moe_bf16* norm_weight, float eps,
+                     const moe_bf16* packed_router, const float* bias, const moe_bf16* packed_w, int64_t T,
+                     moe_bf16* stream_out, moe_bf16* out, int32_t* topk_idx_out, float* topk_w_out,
+                     void* workspace, size_t workspace_bytes, moe_stream_t stream) {
+  int rc = check_T(T);
+  if (rc) return rc;
+  if (T == 0) return MOE_OK;
+  REQUIRE(packed_router && packed_w && out && workspace, "null pointer");
+  REQUIRE(aligned(workspace, 1024), "workspace must be 1024-byte aligned");
+  const size_t need = moe_layer_normed_workspace_bytes(T);
+  if (workspace_bytes < need)
+    return fail(MOE_ERR_WORKSPACE, "moe_layer_normed workspace needs %zu bytes, got %zu", need, workspace_bytes);
+  REQUIRE(aligned(packed_w, 128) && aligned(packed_router, 128), "packed weights must be 128-byte aligned");
+  REQUIRE(aligned(bias, 16) && aligned(out, 16) && aligned(topk_idx_out, 16) && aligned(topk_w_out, 16),
+          "pointers must be 16-byte aligned");
+  const size_t layer = align_up(layer_ws(T, false, 0).total, 1024);
+  moe_bf16* n = reinterpret_cast<moe_bf16*>(static_cast<char*>(workspace) + layer);
+  rc = moe_add_rmsnorm(x, residual, norm_weight, eps, T, kH, MOE_TYPE_BF16, stream_out, MOE_FORMAT_SAME, 0, n,
+                       nullptr, stream);
+  if (rc) return rc;
+  return layer_impl("moe_layer_normed", n, nullptr, packed_router, bias, packed_w, T, residual ? stream_out : x, out,
+                    topk_idx_out, topk_w_out, workspace, layer, stream);
+}
+
+}  // extern "C"

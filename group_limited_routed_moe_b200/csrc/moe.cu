@@ -7,6 +7,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
@@ -15,11 +16,14 @@
 #include "../../include/moe.h"
 #include "combine.cuh"
 #include "common.cuh"
+#include "dense.cuh"
+#include "dense_small.cuh"
 #include "expert_ffn.cuh"
 #include "expert_ffn_skinny.cuh"
 #include "e256.cuh"
 #include "fp4.cuh"
 #include "fp8.cuh"
+#include "norm.cuh"
 #include "pack.cuh"
 #include "permute.cuh"
 #include "route.cuh"
@@ -81,6 +85,8 @@ std::mutex g_dev_mu;
 
 PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
 
+cudaError_t dense_attributes();  // shared-memory limits of the dense products' kernels
+
 int device_setup(int* dev_out, int* sms_out) {
   int dev = 0;
   MOE_CUDA(cudaGetDevice(&dev), "cudaGetDevice");
@@ -129,6 +135,7 @@ int device_setup(int* dev_out, int* sms_out) {
       if (e == cudaSuccess)
         e = cudaFuncSetAttribute(router::router_kernel,
                                  cudaFuncAttributeMaxDynamicSharedMemorySize, router::SMEM_BYTES);
+      if (e == cudaSuccess) e = dense_attributes();
       if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute");
       if (g_encode == nullptr) {
         cudaDriverEntryPointQueryResult q;
@@ -1568,6 +1575,9 @@ extern "C" int moe_permute_fixed_scratch(const int32_t* topk_idx, int64_t T, int
   }
   return do_permute(topk_idx, T, counts, offsets, perm_src, inv_perm, hist, s);
 }
+
+// ---- norm, dense products and the pre-norm layer ------------------------------
+#include "dense_host.cuh"
 
 // ---- explicit per-device set-up ----------------------------------------------
 extern "C" int moe_init_device(void) {

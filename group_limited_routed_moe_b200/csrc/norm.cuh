@@ -1,0 +1,364 @@
+// norm.cuh -- residual addition and root-mean-square norm, with a 16-bit or an
+// 8-bit (int8, FP8 E4M3) output, and its backward pass.
+//
+//   s[t] = round(x[t] + residual[t])                    the new residual stream
+//   y[t][c] = s[t][c] * rstd[t] * w[c],  rstd[t] = 1 / sqrt(mean_c s[t][c]^2 + eps)
+// The norm is taken of the rounded stream, the one that is stored: the
+// backward pass and every later layer see the same values.
+//   8-bit: scale = max(amax |y| / top, 2^-126) over a token's row or over each
+//   128 columns of it, code = round(y / scale), top = 127 (int8) or 448 (E4M3).
+//   backward, with n = s * rstd and dn = dy * w:
+//   dx[t] = rstd (dn - n mean_c(dn n)) + dstream[t],   dw = sum_t dy n
+//
+// Rows whose sum of squares leaves fp32's range are summed again, scaled by a
+// power of two.
+//
+// HBM-bound: a row is read once, kept in registers (fp32 arithmetic, every sum
+// in fp32), and written once.
+#pragma once
+#include <cuda_fp8.h>
+
+#include "common.cuh"
+
+namespace moe {
+namespace norm {
+
+constexpr int kMaxH = 32768;       // a row lives in one block's registers
+constexpr int kMaxParts = 592;     // rows of dw partial sums (4 blocks on each of 148 SMs)
+constexpr int kGroup = 128;        // columns per scale in the grouped form
+
+enum Format { kSame = 0, kInt8 = 1, kE4m3 = 2 };
+
+template <typename E> __device__ __forceinline__ float to_f32(E v);
+template <> __device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
+template <> __device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
+template <typename E> __device__ __forceinline__ E from_f32(float v);
+template <> __device__ __forceinline__ __nv_bfloat16 from_f32(float v) { return __float2bfloat16_rn(v); }
+template <> __device__ __forceinline__ __half from_f32(float v) { return __float2half_rn(v); }
+
+// maximum that keeps a NaN
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+// VEC consecutive elements (16 bytes for VEC = 8, one element for VEC = 1)
+template <typename E, int VEC>
+struct alignas(sizeof(E) * VEC) Pack {
+  E e[VEC];
+};
+
+template <bool MAX>
+__device__ __forceinline__ float combine(float a, float b) {
+  return MAX ? max_nan(a, b) : a + b;
+}
+
+// Sum (or maximum) of v over the block, in a fixed order, returned to every
+// thread.  `red` holds one word per warp; two calls in a row need different ones.
+template <bool MAX>
+__device__ __forceinline__ float block_reduce(float v, float* red) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = combine<MAX>(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+  if (blockDim.x == 32) return v;
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+  __syncthreads();
+  float r = red[0];
+  for (int w = 1; w < static_cast<int>(blockDim.x >> 5); ++w) r = combine<MAX>(r, red[w]);
+  return r;
+}
+
+__device__ __forceinline__ float scale_of(float amax, float top) {
+  return max_nan(__fdiv_rn(amax, top), 1.17549435e-38f);
+}
+
+template <int FMT>
+__device__ __forceinline__ uint8_t code_of(float y, float inv) {
+  if constexpr (FMT == kInt8) {
+    const int q = __float2int_rn(y * inv);
+    return static_cast<uint8_t>(max(-127, min(127, q)));
+  } else {
+    return __nv_cvt_float_to_fp8(y * inv, __NV_SATFINITE, __NV_E4M3);
+  }
+}
+
+// Whether a row's sum of squares left the range in which fp32 holds it well:
+// then the row is scaled by a power of two (row_scale) and summed again.
+__device__ __forceinline__ bool out_of_range(float ss) {
+  return !(ss >= 1e-30f && ss <= 1e38f) && ss != 0.f;
+}
+// The power of two that brings the larger of amax and sqrt(eps) to [1, 2); 1
+// where that is zero, infinite or NaN.
+__device__ __forceinline__ float row_scale(float amax, float eps) {
+  const float c = max_nan(amax, sqrtf(eps));
+  if (!(c > 0.f && c < INFINITY)) return 1.f;
+  return ldexpf(1.f, -max(-126, min(127, ilogbf(c))));
+}
+
+// One row per block; a thread holds NV packs of VEC elements, pack i at column
+// (i * blockDim.x + threadIdx.x) * VEC.  group: 0 (a scale per row) or kGroup.
+template <typename E, int VEC, int NV, int FMT>
+__global__ void __launch_bounds__(1024)
+    add_rmsnorm_kernel(const E* x, const E* res, const E* __restrict__ w, float eps, int H,
+                       int group, E* s_out, void* __restrict__ out, float* __restrict__ scales) {
+  __shared__ float red[3][32];
+  __shared__ unsigned gmax[VEC == 1 ? kMaxH / kGroup : 1];
+  using P = Pack<E, VEC>;
+  griddep_wait();
+  griddep_launch_dependents();
+  const int64_t row = blockIdx.x, base = row * H;
+  const int nvec = H / VEC;
+  float v[NV][VEC];
+  float ss = 0.f;
+  // every load of the row before its first store (s_out may be x or res)
+  P xa[NV], ra[NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int p = i * blockDim.x + threadIdx.x;
+    if (p < nvec) {
+      xa[i] = *reinterpret_cast<const P*>(x + base + static_cast<int64_t>(p) * VEC);
+      if (res != nullptr) ra[i] = *reinterpret_cast<const P*>(res + base + static_cast<int64_t>(p) * VEC);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int p = i * blockDim.x + threadIdx.x;
+    if (p < nvec) {
+      P& a = xa[i];
+      if (res != nullptr) {
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) a.e[j] = from_f32<E>(to_f32(a.e[j]) + to_f32(ra[i].e[j]));
+        *reinterpret_cast<P*>(s_out + base + static_cast<int64_t>(p) * VEC) = a;
+      }
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) {
+        v[i][j] = to_f32(a.e[j]);
+        ss += v[i][j] * v[i][j];
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) v[i][j] = 0.f;
+    }
+  }
+  if (FMT != kSame && VEC == 1 && group) {
+    for (int g = threadIdx.x; g < (H + kGroup - 1) / kGroup; g += blockDim.x) gmax[g] = 0u;
+  }
+  ss = block_reduce<false>(ss, red[0]);
+  float amax = 0.f;
+  if (out_of_range(ss)) {  // the whole block
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) amax = max_nan(amax, fabsf(v[i][j]));
+    const float mult = row_scale(block_reduce<true>(amax, red[1]), eps);
+    if (mult != 1.f) {
+      eps = eps * mult * mult;
+      ss = 0.f;
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) {
+          v[i][j] *= mult;
+          ss += v[i][j] * v[i][j];
+        }
+      ss = block_reduce<false>(ss, red[2]);
+    }
+    __syncthreads();  // red[1] is used again below
+    amax = 0.f;
+  }
+  const float rstd = rsqrtf(ss / static_cast<float>(H) + eps);
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int p = i * blockDim.x + threadIdx.x;
+    if (p < nvec) {
+      P wv;
+      if (w != nullptr) wv = *reinterpret_cast<const P*>(w + static_cast<int64_t>(p) * VEC);
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) {
+        v[i][j] = v[i][j] * rstd * (w != nullptr ? to_f32(wv.e[j]) : 1.f);
+        amax = max_nan(amax, fabsf(v[i][j]));
+      }
+    }
+  }
+  if constexpr (FMT == kSame) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int p = i * blockDim.x + threadIdx.x;
+      if (p < nvec) {
+        P o;
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) o.e[j] = from_f32<E>(v[i][j]);
+        *reinterpret_cast<P*>(static_cast<E*>(out) + base + static_cast<int64_t>(p) * VEC) = o;
+      }
+    }
+  } else {
+    const float top = FMT == kInt8 ? 127.f : 448.f;
+    float scale = 0.f;
+    if (!group) {
+      scale = scale_of(block_reduce<true>(amax, red[1]), top);
+      if (threadIdx.x == 0) scales[row] = scale;
+    } else if constexpr (VEC == 1) {
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int p = i * blockDim.x + threadIdx.x;
+        // non-negative floats (and NaN above them) order like their bits
+        if (p < nvec) atomicMax(&gmax[p / kGroup], __float_as_uint(fabsf(v[i][0])));
+      }
+      __syncthreads();
+    }
+    const int ngroups = (H + kGroup - 1) / kGroup;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int p = i * blockDim.x + threadIdx.x;
+      if (group) {
+        if constexpr (VEC == 1) {
+          if (p < nvec) scale = scale_of(__uint_as_float(gmax[p / kGroup]), top);
+        } else {  // 16 consecutive lanes hold a group's 128 columns
+          float m = 0.f;
+#pragma unroll
+          for (int j = 0; j < VEC; ++j) m = max_nan(m, fabsf(v[i][j]));
+#pragma unroll
+          for (int o = 8; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+          scale = scale_of(m, top);
+        }
+        if (p < nvec && (p * VEC) % kGroup == 0) scales[row * ngroups + p * VEC / kGroup] = scale;
+      }
+      if (p < nvec) {
+        const float inv = 1.f / scale;
+        Pack<uint8_t, VEC> o;
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) o.e[j] = code_of<FMT>(v[i][j], inv);
+        *reinterpret_cast<Pack<uint8_t, VEC>*>(static_cast<uint8_t*>(out) + base +
+                                               static_cast<int64_t>(p) * VEC) = o;
+      }
+    }
+  }
+}
+
+// Rows blockIdx.x, blockIdx.x + gridDim.x, ... ; dw partial sums of a block's
+// rows stay in registers and go to parts[blockIdx.x].
+template <typename E, int VEC, int NV>
+__global__ void __launch_bounds__(1024)
+    rmsnorm_backward_kernel(const E* __restrict__ dy, const E* __restrict__ s,
+                            const E* __restrict__ w, float eps, int64_t T, int H,
+                            const E* __restrict__ dstream, E* __restrict__ dx,
+                            float* __restrict__ parts) {
+  __shared__ float red[3][2][32];
+  using P = Pack<E, VEC>;
+  griddep_wait();
+  griddep_launch_dependents();
+  const int nvec = H / VEC;
+  float dw[NV][VEC];
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) dw[i][j] = 0.f;
+  int flip = 0;
+  for (int64_t row = blockIdx.x; row < T; row += gridDim.x, flip ^= 1) {
+    const int64_t base = row * H;
+    P sv[NV], dv[NV];
+    float ss = 0.f, sd = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int p = i * blockDim.x + threadIdx.x;
+      if (p < nvec) {
+        sv[i] = *reinterpret_cast<const P*>(s + base + static_cast<int64_t>(p) * VEC);
+        dv[i] = *reinterpret_cast<const P*>(dy + base + static_cast<int64_t>(p) * VEC);
+        P wv;
+        if (w != nullptr) wv = *reinterpret_cast<const P*>(w + static_cast<int64_t>(p) * VEC);
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) {
+          const float a = to_f32(sv[i].e[j]);
+          ss += a * a;
+          sd += a * to_f32(dv[i].e[j]) * (w != nullptr ? to_f32(wv.e[j]) : 1.f);
+        }
+      }
+    }
+    // the two sums use other words in every second row, so that a fast warp's
+    // next row does not overwrite what a slow one still reads
+    ss = block_reduce<false>(ss, red[flip][0]);
+    sd = block_reduce<false>(sd, red[flip][1]);
+    float mult = 1.f, amax = 0.f;
+    if (out_of_range(ss)) {  // the whole block: as in the forward pass
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if (i * static_cast<int>(blockDim.x) + static_cast<int>(threadIdx.x) < nvec)
+#pragma unroll
+          for (int j = 0; j < VEC; ++j) amax = max_nan(amax, fabsf(to_f32(sv[i].e[j])));
+      mult = row_scale(block_reduce<true>(amax, red[2][0]), eps);
+      ss = sd = 0.f;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int p = i * blockDim.x + threadIdx.x;
+        if (p < nvec) {
+#pragma unroll
+          for (int j = 0; j < VEC; ++j) {
+            const float a = to_f32(sv[i].e[j]) * mult;
+            ss += a * a;
+            sd += a * to_f32(dv[i].e[j]) *
+                  (w != nullptr ? to_f32(w[static_cast<int64_t>(p) * VEC + j]) : 1.f);
+          }
+        }
+      }
+      __syncthreads();  // every thread has read the first sums
+      ss = block_reduce<false>(ss, red[flip][0]);
+      sd = block_reduce<false>(sd, red[flip][1]);
+    }
+    const float rstd = rsqrtf(ss / static_cast<float>(H) + eps * mult * mult);  // of s * mult
+    const float m = sd * rstd / static_cast<float>(H);                          // mean(dn n)
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int p = i * blockDim.x + threadIdx.x;
+      if (p < nvec) {
+        P wv, ds, o;
+        if (w != nullptr) wv = *reinterpret_cast<const P*>(w + static_cast<int64_t>(p) * VEC);
+        if (dstream != nullptr)
+          ds = *reinterpret_cast<const P*>(dstream + base + static_cast<int64_t>(p) * VEC);
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) {
+          const float n = to_f32(sv[i].e[j]) * mult * rstd, d = to_f32(dv[i].e[j]);
+          dw[i][j] += d * n;
+          float r = rstd * mult * (d * (w != nullptr ? to_f32(wv.e[j]) : 1.f) - n * m);
+          if (dstream != nullptr) r += to_f32(ds.e[j]);
+          o.e[j] = from_f32<E>(r);
+        }
+        *reinterpret_cast<P*>(dx + base + static_cast<int64_t>(p) * VEC) = o;
+      }
+    }
+  }
+  if (parts != nullptr) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int p = i * blockDim.x + threadIdx.x;
+      if (p < nvec) {
+#pragma unroll
+        for (int j = 0; j < VEC; ++j)
+          parts[static_cast<int64_t>(blockIdx.x) * H + static_cast<int64_t>(p) * VEC + j] = dw[i][j];
+      }
+    }
+  }
+}
+
+// dw[c] = sum of parts[0..n)[c], in a fixed order: 32 columns per block, every
+// warp takes each 8th row, then the 8 warps' sums are added.
+__global__ void __launch_bounds__(256)
+    rmsnorm_dw_kernel(const float* __restrict__ parts, int n, int H, float* __restrict__ dw) {
+  __shared__ float sum[8][32];
+  griddep_wait();
+  griddep_launch_dependents();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int c = blockIdx.x * 32 + lane;
+  float a = 0.f;
+  if (c < H)
+    for (int r = warp; r < n; r += 8) a += parts[static_cast<int64_t>(r) * H + c];
+  sum[warp][lane] = a;
+  __syncthreads();
+  if (warp == 0 && c < H) {
+    for (int i = 1; i < 8; ++i) a += sum[i][lane];
+    dw[c] = a;
+  }
+}
+
+}  // namespace norm
+}  // namespace moe

@@ -41,6 +41,7 @@ def _load() -> ctypes.CDLL:
 lib = _load()
 
 _p, _i64, _sz, _i32, _u64 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_size_t, ctypes.c_int, ctypes.c_uint64
+_f32 = ctypes.c_float
 _SIGS = {
     "moe_abi_version": ([], _i32),
     "moe_max_tokens": ([], _i64),
@@ -95,6 +96,16 @@ _SIGS = {
     "moe_expert_ffn_nvfp4_workspace_bytes": ([_i64], _sz),
     "moe_expert_ffn_nvfp4": ([_p, _p, _p, _p, _i64, _p, _p, _p, _sz, _p], _i32),
     "moe_layer_nvfp4": ([_p, _p, _p, _p, _i64, _p, _p, _p, _p, _p, _sz, _p], _i32),
+    "moe_add_rmsnorm": ([_p, _p, _p, _f32, _i64, _i64, _i32, _p, _i32, _i32, _p, _p, _p], _i32),
+    "moe_add_rmsnorm_backward_workspace_bytes": ([_i64, _i64], _sz),
+    "moe_add_rmsnorm_backward": ([_p, _p, _p, _f32, _i64, _i64, _i32, _p, _p, _p, _p, _sz, _p], _i32),
+    "moe_int8_matmul": ([_p, _p, _p, _p, _p, _i64, _i64, _i64, _i32, _p, _p], _i32),
+    "moe_gated_ffn_saved_bytes": ([_i64, _i64], _sz),
+    "moe_gated_ffn": ([_p, _p, _p, _p, _i64, _i64, _i64, _i32, _p, _p, _p, _p, _p], _i32),
+    "moe_gated_ffn_backward_workspace_bytes": ([_i64, _i64], _sz),
+    "moe_gated_ffn_backward": ([_p] * 7 + [_i64, _i64, _i64, _i32] + [_p] * 5 + [_sz, _p], _i32),
+    "moe_layer_normed_workspace_bytes": ([_i64], _sz),
+    "moe_layer_normed": ([_p, _p, _p, _f32, _p, _p, _p, _i64, _p, _p, _p, _p, _p, _sz, _p], _i32),
 }
 for _name, (_args, _ret) in _SIGS.items():
     _f = getattr(lib, _name)
@@ -759,6 +770,249 @@ class HostPipeline:
     def drain(self):
         for st in self.streams():
             st.synchronize()
+
+
+# ----------------------------------------------------------------- norm and dense products
+
+_TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+NORM_FORMATS = {"same": 0, "int8": 1, "e4m3": 2}
+NORM_GROUP = 128
+
+
+def _expect(name: str, t: torch.Tensor, shape, dtype, device) -> None:
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or tuple(t.shape) != tuple(shape) \
+            or not t.is_contiguous() or t.device != device:
+        got = f"{t.dtype} {tuple(t.shape)} on {t.device}" if isinstance(t, torch.Tensor) else repr(t)
+        raise ValueError(f"{name}: expected contiguous {dtype} {tuple(shape)} on {device}, got {got}")
+
+
+def _leading(name: str, t: torch.Tensor, dtypes) -> tuple[torch.device, torch.dtype]:
+    """Device and type of the tensor that sets them for a call."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dim() != 2 or t.dtype not in dtypes \
+            or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous CUDA matrix of {' or '.join(map(str, dtypes))}")
+    return t.device, t.dtype
+
+
+class _on:
+    """Makes a tensor's device current, and on it the stream of the call, so
+    that what the call allocates belongs to that stream."""
+
+    def __init__(self, device, stream):
+        self.device = torch.cuda.device(device)
+        self.stream = stream
+
+    def __enter__(self):
+        self.device.__enter__()
+        self.use = torch.cuda.stream(self.stream) if self.stream is not None else None
+        if self.use is not None:
+            self.use.__enter__()
+        return _stream()
+
+    def __exit__(self, *exc):
+        if self.use is not None:
+            self.use.__exit__(*exc)
+        self.device.__exit__(*exc)
+
+
+def _new(name, t, shape, dtype, device):
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    _expect(name, t, shape, dtype, device)
+    return t
+
+
+def _scratch(name: str, t, nbytes: int, device):
+    """A workspace of at least nbytes bytes (any type), or a fresh one."""
+    if t is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    if not t.is_cuda or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name}: expected contiguous memory on {device}")
+    return t
+
+
+def _nbytes(t) -> int:
+    return 0 if t is None else t.numel() * t.element_size()
+
+
+def moe_add_rmsnorm(x: torch.Tensor, residual: torch.Tensor | None = None, weight=None, eps: float = 1e-6,
+                    out_format: str = "same", group: int = 0, stream_out=None, out=None, scales=None,
+                    stream=None):
+    """s = round(x + residual) and its RMS norm for x [T, H] bf16 or fp16 (see
+    include/moe.h).  Returns (s, out, scales): out in x's type ("same"; scales
+    None), int8 or float8_e4m3fn; scales fp32 [T, 1], or [T, ceil(H / 128)]
+    with group = 128.  Without residual s is x."""
+    dev, dt = _leading("x", x, (torch.bfloat16, torch.float16))
+    if out_format not in NORM_FORMATS:
+        raise ValueError(f"out_format {out_format!r}: one of {sorted(NORM_FORMATS)}")
+    fmt = NORM_FORMATS[out_format]
+    if group not in (0, NORM_GROUP) or (group and not fmt):
+        raise ValueError(f"group {group}: 0, or {NORM_GROUP} with an 8-bit format")
+    T, H = x.shape
+    if residual is not None:
+        _expect("residual", residual, x.shape, dt, dev)
+    if weight is not None:
+        _expect("weight", weight, (H,), dt, dev)
+    with _on(dev, stream) as s:
+        if residual is None:
+            stream_out = x
+        else:
+            stream_out = _new("stream_out", stream_out, x.shape, dt, dev)
+        out = _new("out", out, x.shape, (dt, torch.int8, torch.float8_e4m3fn)[fmt], dev)
+        if fmt:
+            scales = _new("scales", scales, (T, -(-H // group) if group else 1), torch.float32, dev)
+        else:
+            scales = None
+        _check("moe_add_rmsnorm", lib.moe_add_rmsnorm(
+            _ptr(x), _ptr(residual), _ptr(weight), eps, T, H, _TYPES[dt],
+            None if residual is None else _ptr(stream_out), fmt, group, _ptr(out), _ptr(scales), s))
+    return stream_out, out, scales
+
+
+def moe_add_rmsnorm_backward(dy: torch.Tensor, s: torch.Tensor, weight=None, eps: float = 1e-6, dstream=None,
+                             dx=None, dweight=None, need_dweight: bool = True, workspace=None, stream=None):
+    """Gradients of moe_add_rmsnorm's 16-bit form: (dx [T, H], dweight [H] fp32
+    or None); dx is the gradient of x and of residual (see include/moe.h)."""
+    dev, dt = _leading("dy", dy, (torch.bfloat16, torch.float16))
+    T, H = dy.shape
+    _expect("s", s, dy.shape, dt, dev)
+    if weight is not None:
+        _expect("weight", weight, (H,), dt, dev)
+    if dstream is not None:
+        _expect("dstream", dstream, dy.shape, dt, dev)
+    with _on(dev, stream) as st:
+        dx = _new("dx", dx, dy.shape, dt, dev)
+        if need_dweight:
+            dweight = _new("dweight", dweight, (H,), torch.float32, dev)
+            workspace = _scratch("workspace", workspace,
+                                 int(lib.moe_add_rmsnorm_backward_workspace_bytes(T, H)), dev)
+        else:
+            dweight = workspace = None
+        _check("moe_add_rmsnorm_backward", lib.moe_add_rmsnorm_backward(
+            _ptr(dy), _ptr(s), _ptr(weight), eps, T, H, _TYPES[dt], _ptr(dstream), _ptr(dx), _ptr(dweight),
+            _ptr(workspace), _nbytes(workspace), st))
+    return dx, dweight
+
+
+def moe_int8_matmul(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor, b_scale: torch.Tensor,
+                    bias=None, out_dtype: torch.dtype = torch.bfloat16, out=None, stream=None):
+    """[T, N] = (a [T, K] int8 @ b [N, K] int8 transposed) * a_scale [T] (or
+    [T, 1]) * b_scale [N] + bias [N] (see include/moe.h)."""
+    dev, _ = _leading("a", a, (torch.int8,))
+    if not isinstance(b, torch.Tensor) or b.dim() != 2:
+        raise ValueError("b: expected a matrix [N, K]")
+    T, K = a.shape
+    N = b.shape[0]
+    _expect("b", b, (N, K), torch.int8, dev)
+    _expect("a_scale", a_scale, (T, 1) if a_scale.dim() == 2 else (T,), torch.float32, dev)
+    _expect("b_scale", b_scale, (N,), torch.float32, dev)
+    if bias is not None:
+        _expect("bias", bias, (N,), torch.float32, dev)
+    if out_dtype not in _TYPES:
+        raise ValueError(f"out_dtype {out_dtype}: bf16, fp16 or fp32")
+    with _on(dev, stream) as s:
+        out = _new("out", out, (T, N), out_dtype, dev)
+        _check("moe_int8_matmul", lib.moe_int8_matmul(
+            _ptr(a), _ptr(a_scale), _ptr(b), _ptr(b_scale), _ptr(bias), T, N, K, _TYPES[out_dtype], _ptr(out), s))
+    return out
+
+
+def _ffn_shapes(x, w_gate, w_up, w_down):
+    dev, dt = _leading("x", x, (torch.bfloat16, torch.float16))
+    T, H = x.shape
+    if not isinstance(w_gate, torch.Tensor) or w_gate.dim() != 2:
+        raise ValueError("w_gate: expected a matrix [H, I]")
+    I = w_gate.shape[1]
+    for name, w, shape in (("w_gate", w_gate, (H, I)), ("w_up", w_up, (H, I)), ("w_down", w_down, (I, H))):
+        _expect(name, w, shape, dt, dev)
+    return dev, dt, T, H, I
+
+
+def moe_gated_ffn(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, w_down: torch.Tensor,
+                  residual=None, save: bool = False, h=None, y=None, stream=None):
+    """y = round(h W_down + residual), h = round(silu(x W_gate) * (x W_up)), for
+    x [T, H], w_gate and w_up [H, I], w_down [I, H] of one 16-bit type (see
+    include/moe.h).  Returns y, or with save = True (y, saved): what
+    moe_gated_ffn_backward needs of this call."""
+    dev, dt, T, H, I = _ffn_shapes(x, w_gate, w_up, w_down)
+    if residual is not None:
+        _expect("residual", residual, (T, H), dt, dev)
+    with _on(dev, stream) as s:
+        h = _new("h", h, (T, I), dt, dev)
+        y = _new("y", y, (T, H), dt, dev)
+        pre = torch.empty(int(lib.moe_gated_ffn_saved_bytes(T, I)), dtype=torch.uint8, device=dev) if save else None
+        _check("moe_gated_ffn", lib.moe_gated_ffn(
+            _ptr(x), _ptr(w_gate), _ptr(w_up), _ptr(w_down), T, H, I, _TYPES[dt], _ptr(residual), _ptr(h),
+            _ptr(pre), _ptr(y), s))
+    return (y, (h, pre)) if save else y
+
+
+def moe_gated_ffn_backward(dy: torch.Tensor, x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor,
+                           w_down: torch.Tensor, saved, need=(True, True, True, True), dx=None, dw_gate=None,
+                           dw_up=None, dw_down=None, workspace=None, stream=None):
+    """Gradients of moe_gated_ffn: (dx, dw_gate, dw_up, dw_down) in the inputs'
+    type, None where `need` is false; `saved` from the forward call with
+    save = True.  The residual's gradient is dy."""
+    dev, dt, T, H, I = _ffn_shapes(x, w_gate, w_up, w_down)
+    _expect("dy", dy, (T, H), dt, dev)
+    h, pre = saved
+    _expect("saved h", h, (T, I), dt, dev)
+    _expect("saved pre-activations", pre, (int(lib.moe_gated_ffn_saved_bytes(T, I)),), torch.uint8, dev)
+    with _on(dev, stream) as s:
+        outs = [_new(name, t, shape, dt, dev) if want else None
+                for want, name, t, shape in zip(need, ("dx", "dw_gate", "dw_up", "dw_down"),
+                                                (dx, dw_gate, dw_up, dw_down),
+                                                ((T, H), (H, I), (H, I), (I, H)), strict=True)]
+        if any(need[:3]):
+            workspace = _scratch("workspace", workspace,
+                                 int(lib.moe_gated_ffn_backward_workspace_bytes(T, I)), dev)
+        else:
+            workspace = None
+        _check("moe_gated_ffn_backward", lib.moe_gated_ffn_backward(
+            _ptr(dy), _ptr(x), _ptr(w_gate), _ptr(w_up), _ptr(w_down), _ptr(h), _ptr(pre), T, H, I, _TYPES[dt],
+            *(_ptr(t) for t in outs), _ptr(workspace), _nbytes(workspace), s))
+    return tuple(outs)
+
+
+def layer_normed_workspace_bytes(T: int) -> int:
+    return int(lib.moe_layer_normed_workspace_bytes(T))
+
+
+def alloc_layer_normed_workspace(T: int, device) -> torch.Tensor:
+    n = layer_normed_workspace_bytes(T)
+    raw = torch.empty(n + 1024, dtype=torch.uint8, device=device)
+    off = (-raw.data_ptr()) % 1024
+    return raw[off:off + n]
+
+
+def moe_layer_normed(x: torch.Tensor, residual, norm_weight, eps: float, packed_router: torch.Tensor, bias,
+                     packed_w: torch.Tensor, stream_out=None, out=None, topk_idx_out=None, topk_w_out=None,
+                     workspace: torch.Tensor | None = None, stream=None):
+    """The routed layer with its norm in front (see include/moe.h): returns
+    (s, out) with s = round(x + residual), out = round(s + MoE(RMSNorm(s)))."""
+    dev, _ = _leading("x", x, (torch.bfloat16,))
+    T = x.shape[0]
+    _expect("x", x, (T, HIDDEN), torch.bfloat16, dev)
+    for name, t, shape, dt in (("residual", residual, (T, HIDDEN), torch.bfloat16),
+                               ("norm_weight", norm_weight, (HIDDEN,), torch.bfloat16),
+                               ("bias", bias, (N_EXPERTS,), torch.float32),
+                               ("topk_idx_out", topk_idx_out, (T, TOPK), torch.int32),
+                               ("topk_w_out", topk_w_out, (T, TOPK), torch.float32)):
+        if t is not None:
+            _expect(name, t, shape, dt, dev)
+    with _on(dev, stream) as s:
+        if residual is None:
+            stream_out = x
+        else:
+            stream_out = _new("stream_out", stream_out, x.shape, torch.bfloat16, dev)
+        out = _new("out", out, x.shape, torch.bfloat16, dev)
+        if workspace is None:
+            workspace = alloc_layer_normed_workspace(T, dev)
+        _check("moe_layer_normed", lib.moe_layer_normed(
+            _ptr(x), _ptr(residual), _ptr(norm_weight), eps, _ptr(packed_router), _ptr(bias), _ptr(packed_w), T,
+            None if residual is None else _ptr(stream_out), _ptr(out), _ptr(topk_idx_out), _ptr(topk_w_out),
+            _ptr(workspace), _nbytes(workspace), s))
+    return stream_out, out
 
 
 # ----------------------------------------------------------------- status

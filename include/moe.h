@@ -629,6 +629,115 @@ int moe_permute_fixed_scratch(const int32_t* topk_idx, int64_t T, int32_t* count
                               int32_t* offsets, int32_t* perm_src, int32_t* inv_perm,
                               moe_stream_t stream);
 
+/* ---- norm, dense feed-forward block, 8-bit products --------------------------- */
+
+/* What stands around the routed layers: every layer's feed-forward step begins
+ * with the residual stream's addition and norm, and the model's first layer is
+ * dense ("Ling-3.0-tiny on a Qualcomm board", TensorFold issue #1247, first
+ * comment: dense layer 0).  Sizes are arguments here; arrays are dense
+ * row-major and 16-byte aligned.  An element type is one of these codes. */
+typedef enum moe_type { MOE_TYPE_BF16 = 0, MOE_TYPE_F16 = 1, MOE_TYPE_F32 = 2 } moe_type;
+
+/* Output of moe_add_rmsnorm: the input's type, or 8-bit codes with scales. */
+typedef enum moe_format { MOE_FORMAT_SAME = 0, MOE_FORMAT_INT8 = 1, MOE_FORMAT_E4M3 = 2 } moe_format;
+
+/* Residual addition and root-mean-square norm:
+ *   s[t] = round(x[t] + residual[t])  (one rounding; x itself without residual)
+ *   y[t][c] = s[t][c] * weight[c] / sqrt(mean_c s[t][c]^2 + eps)
+ * in fp32 (rows whose sum of squares leaves its range are scaled first).
+ *   x, residual : [T][H] of `dtype` (bf16 or fp16); residual may be NULL
+ *   weight      : [H] of `dtype`, or NULL for ones
+ *   stream_out  : [T][H] (out), s; required with residual, not written without.
+ *                 May be x or residual.
+ *   format      : MOE_FORMAT_SAME: out [T][H] of `dtype`, scales not used;
+ *                 MOE_FORMAT_INT8: out [T][H] int8 in [-127, 127];
+ *                 MOE_FORMAT_E4M3: out [T][H] FP8 E4M3 (at most +-448).
+ *   group       : 0, or 128 (8-bit formats): columns that share a scale, 0 the
+ *                 whole row; the last group of a row may be shorter.
+ *   scales      : fp32 [T][1] or [T][ceil(H / 128)] (out): max(amax |y| / top,
+ *                 2^-126), top 127 or 448; a value is code * scale, codes are
+ *                 rounded to nearest.  A NaN in a row or group makes its scale
+ *                 NaN.
+ * 1 <= H <= 32768; rows of H % 8 == 0 take 16-byte accesses. */
+int moe_add_rmsnorm(const void* x, const void* residual, const void* weight, float eps, int64_t T,
+                    int64_t H, int dtype, void* stream_out, int format, int group, void* out,
+                    float* scales, moe_stream_t stream);
+
+/* Scratch bytes moe_add_rmsnorm_backward needs (with dweight; 0 without). */
+size_t moe_add_rmsnorm_backward_workspace_bytes(int64_t T, int64_t H);
+
+/* Gradients of moe_add_rmsnorm with MOE_FORMAT_SAME.
+ *   dy      : [T][H] gradient of y;  s: [T][H] the stream the norm was taken of
+ *   dstream : [T][H] gradient that reaches s from elsewhere, added; or NULL
+ *   dx      : [T][H] (out) gradient of s, which is that of x and of residual
+ *   dweight : fp32 [H] (out), or NULL.  Summed in a fixed order.
+ * dy, s, weight, dstream and dx are of `dtype`; dx must alias no input.
+ * T == 0 sets dweight to zero. */
+int moe_add_rmsnorm_backward(const void* dy, const void* s, const void* weight, float eps, int64_t T,
+                             int64_t H, int dtype, const void* dstream, void* dx, float* dweight,
+                             void* workspace, size_t workspace_bytes, moe_stream_t stream);
+
+/* Matrix product in 8-bit integers, a scale for each token and each channel:
+ *   out[t][n] = (sum_k a[t][k] b[n][k]) * a_scale[t] * b_scale[n] + bias[n]
+ * with exact int32 sums; the rest in fp32, rounded once.
+ *   a : [T][K] int8, a_scale : [T] fp32 (moe_add_rmsnorm's INT8 output, group 0)
+ *   b : [N][K] int8 ([out, in] orientation), b_scale : [N] fp32
+ *   bias : [N] fp32 or NULL;  out : [T][N] bf16, fp16 or fp32 (out_dtype)
+ * K a multiple of 16 in [16, 131056], 1 <= N <= 2^20. */
+int moe_int8_matmul(const int8_t* a, const float* a_scale, const int8_t* b, const float* b_scale,
+                    const float* bias, int64_t T, int64_t N, int64_t K, int out_dtype, void* out,
+                    moe_stream_t stream);
+
+/* Bytes of the pre-activations moe_gated_ffn saves for its backward pass: the
+ * upper 24 bits of the fp32 x W_gate and x W_up (6 T I bytes). */
+size_t moe_gated_ffn_saved_bytes(int64_t T, int64_t I);
+
+/* The gated feed-forward block of any width (the routed experts' FFN, dense):
+ *   h = round(silu(x W_gate) * (x W_up)),  y = round(h W_down + residual)
+ * with fp32 accumulation, in two launches.  All matrices of one 16-bit `dtype`
+ * (bf16 or fp16), as they are (no packing):
+ *   x : [T][H];  w_gate, w_up : [H][I];  w_down : [I][H]
+ *   residual : [T][H] or NULL;  h : [T][I] (out);  y : [T][H] (out)
+ *   saved    : moe_gated_ffn_saved_bytes(T, I) bytes (out), or NULL when no
+ *              backward pass follows
+ * y may be x or residual.  H and I multiples of 8 in [8, 65536]. */
+int moe_gated_ffn(const void* x, const void* w_gate, const void* w_up, const void* w_down, int64_t T,
+                  int64_t H, int64_t I, int dtype, const void* residual, void* h, void* saved, void* y,
+                  moe_stream_t stream);
+
+/* Scratch bytes moe_gated_ffn_backward needs (dg and du, 4 T I). */
+size_t moe_gated_ffn_backward_workspace_bytes(int64_t T, int64_t I);
+
+/* Gradients of moe_gated_ffn from dy [T][H] (that of the residual is dy), with
+ * g = x W_gate, u = x W_up:
+ *   dh = dy W_down^T, du = round(dh silu(g)), dg = round(dh u silu'(g))
+ *   dx = dg W_gate^T + du W_up^T
+ *   dw_gate = x^T dg, dw_up = x^T du, dw_down = h^T dy
+ * h and saved from the forward call; outputs of `dtype`, shapes as the inputs',
+ * each may be NULL (not computed).  Inputs that no wanted output needs may be
+ * NULL, and the workspace when dw_down alone is wanted.  No output may alias
+ * an input or the workspace.  Every sum in a fixed order.  T == 0 sets the
+ * weights' gradients to zero. */
+int moe_gated_ffn_backward(const void* dy, const void* x, const void* w_gate, const void* w_up,
+                           const void* w_down, const void* h, const void* saved, int64_t T, int64_t H,
+                           int64_t I, int dtype, void* dx, void* dw_gate, void* dw_up, void* dw_down,
+                           void* workspace, size_t workspace_bytes, moe_stream_t stream);
+
+/* Workspace bytes moe_layer_normed needs: moe_layer's, and the normed rows. */
+size_t moe_layer_normed_workspace_bytes(int64_t T);
+
+/* A routed layer as it stands in the model, its norm in front:
+ *   s = bf16(x + residual), n = RMSNorm(s) (moe_add_rmsnorm)
+ *   out = bf16(s + MoE(n)), routed from n by packed_router (moe_layer_routed)
+ *   x, residual : [T][1536] bf16; residual may be NULL (then s = x)
+ *   norm_weight : [1536] bf16 or NULL;  stream_out : [T][1536] (out), s; required
+ *                 with residual, not written without.  May be x or residual.
+ * Other arguments as in moe_layer_routed; out may be x, residual or stream_out. */
+int moe_layer_normed(const moe_bf16* x, const moe_bf16* residual, const moe_bf16* norm_weight, float eps,
+                     const moe_bf16* packed_router, const float* bias, const moe_bf16* packed_w, int64_t T,
+                     moe_bf16* stream_out, moe_bf16* out, int32_t* topk_idx_out, float* topk_w_out,
+                     void* workspace, size_t workspace_bytes, moe_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
