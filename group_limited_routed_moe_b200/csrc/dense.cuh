@@ -39,16 +39,24 @@ enum Type { kBF16 = 0, kF16 = 1, kF32 = 2 };             // 16-bit operand type 
 constexpr int kKB = 128;                                  // bytes of k per k-block
 
 // The saved pre-activations of the gated block: the upper 24 bits of the fp32
-// g and u (mantissa cut to 16 bits, relative error below 2^-15), as three
-// [T][I] planes of 16-bit words: g's upper half, u's upper half, and their
-// next 8 bits (g's in the low byte).  Rounding them to 16 bits instead would
-// cost the gradients a third rounding of the size of the operands' own.
-struct Saved {
-  uint16_t *g, *u, *lo;
-};
-struct SavedIn {
-  const uint16_t *g, *u, *lo;
-};
+// g and u (mantissa cut to 15 bits, relative error below 2^-15).  Rounding them
+// to 16 bits instead would cost the gradients a third rounding of the size of
+// the operands' own.  They lie in blocks of 32 x 32, row-block-major, as three
+// planes of 16-bit words: g's upper half, u's upper half, their next 8 bits
+// (g's in the low byte).  Inside a plane 8 columns of a row are 16 consecutive
+// bytes and the 32 rows of these follow one another, so that a warp with a row
+// in each lane, as the accumulators come, reads and writes 512 bytes at a time.
+constexpr int kSavedPlane = 2048, kSavedBlock = 3 * kSavedPlane;
+__host__ __device__ constexpr int64_t saved_bytes(int64_t T, int64_t I) {
+  return ((T + 31) / 32) * ((I + 31) / 32) * kSavedBlock;
+}
+__device__ __forceinline__ int64_t saved_block(int64_t row, int64_t col, int64_t I) {
+  return ((row >> 5) * ((I + 31) >> 5) + (col >> 5)) * kSavedBlock;
+}
+// Offset of an element's word inside its block's plane.
+__device__ __forceinline__ int saved_word(int64_t row, int64_t col) {
+  return static_cast<int>(((col & 31) >> 3) * 512 + (row & 31) * 16 + (col & 7) * 2);
+}
 
 struct Problem {
   int64_t M, N;   // rows and columns of the output
@@ -68,8 +76,7 @@ struct Args {
   int type;        // 16-bit type of operands and outputs (Type), or kF32 outputs (kScaled)
   uint32_t idesc;
   const uint16_t* residual;        // kPlain: [M][N] or NULL
-  Saved saved;                     // kGated: planes to write (g NULL: none)
-  SavedIn in;                      // kDGate: planes to read
+  uint8_t* saved;                  // pre-activations: kGated writes them (NULL: no), kDGate reads
   void* out2;                      // kDGate: du (p[0].out is dg)
   const float *a_scale, *b_scale, *bias;  // kScaled
   bool vec;                        // output rows are 16-byte aligned
@@ -202,11 +209,33 @@ __device__ __forceinline__ float unpack1(uint16_t v, int type) {
   return type == kF16 ? __half2float(__ushort_as_half(v)) : __uint_as_float(uint32_t(v) << 16);
 }
 
-// silu and the two factors of its gradient.  For very negative g the
-// exponential overflows to infinity and sigma is 0, the limit; the products
-// with it stay finite.
+// For very negative g the exponential overflows to infinity and the quotient
+// is 0, the limit.
 __device__ __forceinline__ float sigmoid(float g) { return __fdividef(1.0f, 1.0f + __expf(-g)); }
 __device__ __forceinline__ float silu(float g) { return __fdividef(g, 1.0f + __expf(-g)); }
+
+// Gradients of silu(g) * u: du = dh silu(g), dg = dh u silu'(g).
+__device__ __forceinline__ void dgate(float dh, float g, float u, float& dg, float& du) {
+  const float s = sigmoid(g), act = g * s;
+  du = dh * act;
+  dg = dh * u * (s + act * (1.f - s));
+}
+
+// 32 consecutive fp32 columns of the calling warp's 32 TMEM lanes.
+__device__ __forceinline__ void tmem_ld_32(uint32_t taddr, uint32_t (&a)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(a[0]), "=r"(a[1]), "=r"(a[2]), "=r"(a[3]), "=r"(a[4]), "=r"(a[5]), "=r"(a[6]),
+        "=r"(a[7]), "=r"(a[8]), "=r"(a[9]), "=r"(a[10]), "=r"(a[11]), "=r"(a[12]), "=r"(a[13]),
+        "=r"(a[14]), "=r"(a[15]), "=r"(a[16]), "=r"(a[17]), "=r"(a[18]), "=r"(a[19]),
+        "=r"(a[20]), "=r"(a[21]), "=r"(a[22]), "=r"(a[23]), "=r"(a[24]), "=r"(a[25]),
+        "=r"(a[26]), "=r"(a[27]), "=r"(a[28]), "=r"(a[29]), "=r"(a[30]), "=r"(a[31])
+      : "r"(taddr)
+      : "memory");
+}
 
 // ---------------------------------------------------------------- block stores
 
@@ -218,7 +247,7 @@ constexpr int kStageWarp = 32 * kStageRow;     // one warp's block
 // each row leaves as one 64-byte segment.  nrows rows and `ncols` columns
 // (elements of ES bytes) of it exist.  Rows that are not 16-byte aligned go
 // out element by element, lanes along the row.
-template <int ES>
+template <int ES, bool ALWAYS_VEC>
 __device__ __forceinline__ void store_block(const uint32_t* pk, uint32_t stage, uint8_t* g0,
                                             int64_t ld_bytes, int nrows, int64_t ncols, bool vec,
                                             int lane) {
@@ -227,7 +256,7 @@ __device__ __forceinline__ void store_block(const uint32_t* pk, uint32_t stage, 
   for (int q = 0; q < 4; ++q)
     st_shared_v4(mine + q * 16, pk[4 * q], pk[4 * q + 1], pk[4 * q + 2], pk[4 * q + 3]);
   __syncwarp();
-  if (vec) {
+  if (ALWAYS_VEC || vec) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int row = i * 8 + (lane >> 2), ch = lane & 3;
@@ -450,121 +479,126 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
         break;
       tc_fence_after();
       const uint32_t d = tmem + a * BN + (uint32_t(quarter * 32) << 16);
-      uint32_t x0[32], x1[32];
-      if constexpr (EPI == kGated) {
-        constexpr int W = BN / 4;  // output columns of this warp
+      // this warp's half of the columns, 32 at a time; after the last tensor
+      // memory read the accumulators go back to the MMAs
+      constexpr int W = EPI == kGated ? BN / 4 : BN / 2;
 #pragma unroll 1
-        for (int c = 0; c < W; c += 32) {
-          const int lc = half * W + c;
-          tmem_ld_2x32(d + lc, d + BN / 2 + lc, x0, x1);
-          if (c + 32 >= W) {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(map_to_rank(smem_u32(&S->tempty[a]), 0));
+      for (int c = 0; c < W; c += 32) {
+        const int lc = half * W + c;
+        const int64_t col = int64_t(n) * (EPI == kGated ? BN / 2 : BN) + lc, left = P.N - col;
+        const bool any = left > 0 && nrows > 0;
+        uint4 gh[4], uh[4], lo[4];
+        if constexpr (EPI == kDGate) {
+          if (any) {
+            const uint4* sv = reinterpret_cast<const uint4*>(g.saved + saved_block(row0, col, P.N)) + lane;
+#pragma unroll
+            for (int q4 = 0; q4 < 4; ++q4) {
+              gh[q4] = sv[q4 * 32];
+              uh[q4] = sv[(4 + q4) * 32];
+              lo[q4] = sv[(8 + q4) * 32];
+            }
           }
-          const int64_t col = int64_t(n) * (BN / 2) + lc, left = P.N - col;
-          if (left <= 0) continue;
-          const int64_t at = row0 * P.N + col;
-          uint32_t pk[16];
-          if (g.saved.g != nullptr) {
+        }
+        uint32_t x[32], x1[EPI == kGated ? 32 : 1];
+        if constexpr (EPI == kGated)
+          tmem_ld_2x32(d + lc, d + BN / 2 + lc, x, x1);
+        else
+          tmem_ld_32(d + lc, x);
+        if (c + 32 >= W) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(map_to_rank(smem_u32(&S->tempty[a]), 0));
+        }
+        if (!any) continue;
+        const int64_t at = row0 * P.N + col;
+        uint32_t pk[16];
+        if constexpr (EPI == kGated) {
+          if (g.saved != nullptr) {
+            uint4* sv = reinterpret_cast<uint4*>(g.saved + saved_block(row0, col, P.N)) + lane;
+            auto hi = [](uint32_t e, uint32_t o) { return (e >> 16) | (o & 0xFFFF0000u); };
+            auto mid = [](uint32_t ge, uint32_t ue, uint32_t go, uint32_t uo) {
+              return ((ge >> 8) & 0xFFu) | (ue & 0xFF00u) | ((go << 8) & 0xFF0000u) | ((uo << 16) & 0xFF000000u);
+            };
 #pragma unroll
-            for (int i = 0; i < 16; ++i) pk[i] = (x0[2 * i] >> 16) | (x0[2 * i + 1] & 0xFFFF0000u);
-            store_block<2>(pk, stage, reinterpret_cast<uint8_t*>(g.saved.g + at), P.N * 2, nrows, left, g.vec, lane);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) pk[i] = (x1[2 * i] >> 16) | (x1[2 * i + 1] & 0xFFFF0000u);
-            store_block<2>(pk, stage, reinterpret_cast<uint8_t*>(g.saved.u + at), P.N * 2, nrows, left, g.vec, lane);
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-              pk[i] = ((x0[2 * i] >> 8) & 0xFFu) | (x1[2 * i] & 0xFF00u) |
-                      ((x0[2 * i + 1] << 8) & 0xFF0000u) | ((x1[2 * i + 1] << 16) & 0xFF000000u);
-            store_block<2>(pk, stage, reinterpret_cast<uint8_t*>(g.saved.lo + at), P.N * 2, nrows, left, g.vec, lane);
+            for (int q4 = 0; q4 < 4; ++q4) {
+              const uint32_t *e = x + 8 * q4, *f = x1 + 8 * q4;
+              sv[q4 * 32] = make_uint4(hi(e[0], e[1]), hi(e[2], e[3]), hi(e[4], e[5]), hi(e[6], e[7]));
+              sv[(4 + q4) * 32] = make_uint4(hi(f[0], f[1]), hi(f[2], f[3]), hi(f[4], f[5]), hi(f[6], f[7]));
+              sv[(8 + q4) * 32] = make_uint4(mid(e[0], f[0], e[1], f[1]), mid(e[2], f[2], e[3], f[3]),
+                                             mid(e[4], f[4], e[5], f[5]), mid(e[6], f[6], e[7], f[7]));
+            }
           }
 #pragma unroll
           for (int i = 0; i < 16; ++i)
-            pk[i] = pack2(silu(__uint_as_float(x0[2 * i])) * __uint_as_float(x1[2 * i]),
-                          silu(__uint_as_float(x0[2 * i + 1])) * __uint_as_float(x1[2 * i + 1]), g.type);
-          store_block<2>(pk, stage, static_cast<uint8_t*>(P.out) + at * 2, P.N * 2, nrows, left, g.vec, lane);
-        }
-      } else {
-        constexpr int W = BN / 2;
-#pragma unroll 1
-        for (int c = 0; c < W; c += 64) {
-          const int lc = half * W + c;
-          tmem_ld_2x32(d + lc, d + lc + 32, x0, x1);
-          if (c + 64 >= W) {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(map_to_rank(smem_u32(&S->tempty[a]), 0));
+            pk[i] = pack2(silu(__uint_as_float(x[2 * i])) * __uint_as_float(x1[2 * i]),
+                          silu(__uint_as_float(x[2 * i + 1])) * __uint_as_float(x1[2 * i + 1]), g.type);
+          store_block<2, true>(pk, stage, static_cast<uint8_t*>(P.out) + at * 2, P.N * 2, nrows, left, true, lane);
+        } else if constexpr (EPI == kPlain) {
+          if (g.residual != nullptr) {
+            uint32_t r[16];
+            load_row32(g.residual + at + lane * P.N, row_ok, left, r);
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              pk[i] = pack2(__uint_as_float(x[2 * i]) + unpack_lo(r[i], g.type),
+                            __uint_as_float(x[2 * i + 1]) + unpack_hi(r[i], g.type), g.type);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              pk[i] = pack2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]), g.type);
           }
+          store_block<2, true>(pk, stage, static_cast<uint8_t*>(P.out) + at * 2, P.N * 2, nrows, left, true, lane);
+        } else if constexpr (EPI == kDGate) {
+          uint32_t pg[16];
 #pragma unroll
-          for (int hh = 0; hh < 2; ++hh) {
-            uint32_t(&x)[32] = hh ? x1 : x0;
-            const int64_t col = int64_t(n) * BN + lc + hh * 32, left = P.N - col;
-            if (left <= 0) continue;
-            const int64_t at = row0 * P.N + col;
-            uint32_t pk[16];
-            if constexpr (EPI == kPlain) {
-              if (g.residual != nullptr) {
-                uint32_t r[16];
-                load_row32(g.residual + at + lane * P.N, row_ok, left, r);
+          for (int i = 0; i < 16; ++i) {
+            const uint32_t hw = (&gh[i / 4].x)[i % 4], uw = (&uh[i / 4].x)[i % 4], lw = (&lo[i / 4].x)[i % 4];
+            float dg[2], du[2];
 #pragma unroll
-                for (int i = 0; i < 16; ++i)
-                  pk[i] = pack2(__uint_as_float(x[2 * i]) + unpack_lo(r[i], g.type),
-                                __uint_as_float(x[2 * i + 1]) + unpack_hi(r[i], g.type), g.type);
-              } else {
+            for (int j = 0; j < 2; ++j) {
+              const uint32_t l = lw >> (16 * j);
+              const float gg = __uint_as_float((j ? hw & 0xFFFF0000u : hw << 16) | ((l & 0xFFu) << 8));
+              const float uu = __uint_as_float((j ? uw & 0xFFFF0000u : uw << 16) | (l & 0xFF00u));
+              dgate(__uint_as_float(x[2 * i + j]), gg, uu, dg[j], du[j]);
+            }
+            pg[i] = pack2(dg[0], dg[1], g.type);
+            pk[i] = pack2(du[0], du[1], g.type);
+          }
+          store_block<2, true>(pg, stage, static_cast<uint8_t*>(P.out) + at * 2, P.N * 2, nrows, left, true, lane);
+          store_block<2, true>(pk, stage, static_cast<uint8_t*>(g.out2) + at * 2, P.N * 2, nrows, left, true, lane);
+        } else {
+          const float sa = row_ok ? g.a_scale[row] : 0.f;
+          if (left >= 32) {  // the scales of 32 columns, the same for every lane
 #pragma unroll
-                for (int i = 0; i < 16; ++i)
-                  pk[i] = pack2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]), g.type);
-              }
-              store_block<2>(pk, stage, static_cast<uint8_t*>(P.out) + at * 2, P.N * 2, nrows, left, g.vec, lane);
-            } else if constexpr (EPI == kDGate) {
-              uint32_t gh[16], uh[16], lo[16], pg[16];
-              load_row32(g.in.g + at + lane * P.N, row_ok, left, gh);
-              load_row32(g.in.u + at + lane * P.N, row_ok, left, uh);
-              load_row32(g.in.lo + at + lane * P.N, row_ok, left, lo);
+            for (int i = 0; i < 8; ++i) {
+              const float4 sb = *reinterpret_cast<const float4*>(g.b_scale + col + 4 * i);
+              float4 bi = make_float4(0.f, 0.f, 0.f, 0.f);
+              if (g.bias != nullptr) bi = *reinterpret_cast<const float4*>(g.bias + col + 4 * i);
 #pragma unroll
-              for (int i = 0; i < 16; ++i) {
-                float dg[2], du[2];
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                  const uint32_t l = lo[i] >> (16 * j);
-                  const float gg = __uint_as_float((j ? gh[i] & 0xFFFF0000u : gh[i] << 16) | ((l & 0xFFu) << 8));
-                  const float uu = __uint_as_float((j ? uh[i] & 0xFFFF0000u : uh[i] << 16) | (l & 0xFF00u));
-                  const float dh = __uint_as_float(x[2 * i + j]);
-                  const float sg = sigmoid(gg), act = silu(gg);
-                  du[j] = dh * act;
-                  dg[j] = dh * uu * (sg + act * (1.f - sg));
-                }
-                pg[i] = pack2(dg[0], dg[1], g.type);
-                pk[i] = pack2(du[0], du[1], g.type);
-              }
-              store_block<2>(pg, stage, static_cast<uint8_t*>(P.out) + at * 2, P.N * 2, nrows, left, g.vec, lane);
-              store_block<2>(pk, stage, static_cast<uint8_t*>(g.out2) + at * 2, P.N * 2, nrows, left, g.vec, lane);
-            } else {
-              const float sa = row_ok ? g.a_scale[row] : 0.f;
-              float y[32];
-#pragma unroll
-              for (int i = 0; i < 32; ++i) {
-                const bool in = i < left;
-                const float sb = in ? g.b_scale[col + i] : 0.f;
-                y[i] = static_cast<float>(static_cast<int>(x[i])) * sa * sb;
-                if (g.bias != nullptr && in) y[i] += g.bias[col + i];
-              }
-              if (g.type == kF32) {
-#pragma unroll
-                for (int f = 0; f < 2; ++f) {
-#pragma unroll
-                  for (int i = 0; i < 16; ++i) pk[i] = __float_as_uint(y[f * 16 + i]);
-                  if (left > f * 16)
-                    store_block<4>(pk, stage, static_cast<uint8_t*>(P.out) + (at + f * 16) * 4, P.N * 4, nrows,
-                                   left - f * 16, g.vec, lane);
-                }
-              } else {
-#pragma unroll
-                for (int i = 0; i < 16; ++i) pk[i] = pack2(y[2 * i], y[2 * i + 1], g.type);
-                store_block<2>(pk, stage, static_cast<uint8_t*>(P.out) + at * 2, P.N * 2, nrows, left, g.vec, lane);
+              for (int j = 0; j < 4; ++j) {
+                uint32_t& v = x[4 * i + j];
+                v = __float_as_uint(fmaf(static_cast<float>(static_cast<int>(v)) * sa, (&sb.x)[j], (&bi.x)[j]));
               }
             }
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              const bool in = i < left;
+              const float sb = in ? g.b_scale[col + i] : 0.f;
+              const float bi = in && g.bias != nullptr ? g.bias[col + i] : 0.f;
+              x[i] = __float_as_uint(fmaf(static_cast<float>(static_cast<int>(x[i])) * sa, sb, bi));
+            }
+          }
+          if (g.type == kF32) {
+#pragma unroll
+            for (int f = 0; f < 2; ++f)
+              if (left > f * 16)
+                store_block<4, false>(x + f * 16, stage, static_cast<uint8_t*>(P.out) + (at + f * 16) * 4, P.N * 4,
+                                      nrows, left - f * 16, g.vec, lane);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              pk[i] = pack2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]), g.type);
+            store_block<2, false>(pk, stage, static_cast<uint8_t*>(P.out) + at * 2, P.N * 2, nrows, left, g.vec, lane);
           }
         }
       }

@@ -21,32 +21,39 @@ RowShape row_shape(int64_t nvec) {
   return {static_cast<int>((per + 31) / 32 * 32), nv};
 }
 
-template <typename E, int VEC, int NV>
-int launch_norm_fmt(int fmt, const RowShape& rs, int64_t T, const void* x, const void* res, const void* w,
-                    float eps, int H, int group, void* s_out, void* out, float* scales, cudaStream_t s) {
-  auto k = fmt == norm::kSame   ? norm::add_rmsnorm_kernel<E, VEC, NV, norm::kSame>
-           : fmt == norm::kInt8 ? norm::add_rmsnorm_kernel<E, VEC, NV, norm::kInt8>
-                                : norm::add_rmsnorm_kernel<E, VEC, NV, norm::kE4m3>;
-  return launch_pdl("add_rmsnorm_kernel launch", k, dim3(static_cast<unsigned>(T)), dim3(rs.threads), 0, s,
-                    static_cast<const E*>(x), static_cast<const E*>(res), static_cast<const E*>(w), eps, H,
-                    group, static_cast<E*>(s_out), out, scales);
+// f(std::integral_constant<int, NV>, std::integral_constant<int, MAXT>) for the
+// kernel that holds rows of that shape: the largest block it is compiled for is
+// 256 threads up to 4 packs a thread (so that it may use the registers), 1024 above.
+template <int VEC, typename F>
+int with_row_shape(const RowShape& rs, F&& f) {
+  using std::integral_constant;
+  if (rs.threads <= 256) {
+    if (rs.nv == 1) return f(integral_constant<int, 1>{}, integral_constant<int, 256>{});
+    if (rs.nv == 2) return f(integral_constant<int, 2>{}, integral_constant<int, 256>{});
+    if (rs.nv == 4) return f(integral_constant<int, 4>{}, integral_constant<int, 256>{});
+  }
+  if (rs.nv == 4) return f(integral_constant<int, 4>{}, integral_constant<int, 1024>{});
+  if constexpr (VEC == 1) {
+    if (rs.nv == 8) return f(integral_constant<int, 8>{}, integral_constant<int, 1024>{});
+    if (rs.nv == 16) return f(integral_constant<int, 16>{}, integral_constant<int, 1024>{});
+    if (rs.nv == 32) return f(integral_constant<int, 32>{}, integral_constant<int, 1024>{});
+  }
+  return fail(MOE_ERR_INVALID_ARG, "row of %d x %d packs", rs.threads, rs.nv);
 }
+
 template <typename E, int VEC>
 int launch_norm(int fmt, int64_t T, const void* x, const void* res, const void* w, float eps, int H,
                 int group, void* s_out, void* out, float* scales, cudaStream_t s) {
   const RowShape rs = row_shape(H / VEC);
-  switch (rs.nv) {
-    case 1: return launch_norm_fmt<E, VEC, 1>(fmt, rs, T, x, res, w, eps, H, group, s_out, out, scales, s);
-    case 2: return launch_norm_fmt<E, VEC, 2>(fmt, rs, T, x, res, w, eps, H, group, s_out, out, scales, s);
-    case 4: return launch_norm_fmt<E, VEC, 4>(fmt, rs, T, x, res, w, eps, H, group, s_out, out, scales, s);
-    default: break;
-  }
-  if constexpr (VEC == 1) {
-    if (rs.nv == 8) return launch_norm_fmt<E, 1, 8>(fmt, rs, T, x, res, w, eps, H, group, s_out, out, scales, s);
-    if (rs.nv == 16) return launch_norm_fmt<E, 1, 16>(fmt, rs, T, x, res, w, eps, H, group, s_out, out, scales, s);
-    if (rs.nv == 32) return launch_norm_fmt<E, 1, 32>(fmt, rs, T, x, res, w, eps, H, group, s_out, out, scales, s);
-  }
-  return fail(MOE_ERR_INVALID_ARG, "H=%d", H);
+  return with_row_shape<VEC>(rs, [&](auto nv, auto maxt) {
+    constexpr int NV = decltype(nv)::value, MAXT = decltype(maxt)::value;
+    auto k = fmt == norm::kSame   ? norm::add_rmsnorm_kernel<E, VEC, NV, norm::kSame, MAXT>
+             : fmt == norm::kInt8 ? norm::add_rmsnorm_kernel<E, VEC, NV, norm::kInt8, MAXT>
+                                  : norm::add_rmsnorm_kernel<E, VEC, NV, norm::kE4m3, MAXT>;
+    return launch_pdl("add_rmsnorm_kernel launch", k, dim3(static_cast<unsigned>(T)), dim3(rs.threads), 0, s,
+                      static_cast<const E*>(x), static_cast<const E*>(res), static_cast<const E*>(w), eps, H,
+                      group, static_cast<E*>(s_out), out, scales);
+  });
 }
 
 int do_add_rmsnorm(int type, int fmt, int64_t T, const void* x, const void* res, const void* w, float eps,
@@ -63,26 +70,24 @@ template <typename E, int VEC>
 int launch_norm_bwd(int64_t T, const void* dy, const void* sv, const void* w, float eps, int H,
                     const void* dstream, void* dx, float* parts, int blocks, cudaStream_t s) {
   const RowShape rs = row_shape(H / VEC);
-  auto go = [&](auto k) {
-    return launch_pdl("rmsnorm_backward_kernel launch", k, dim3(blocks), dim3(rs.threads), 0, s,
-                      static_cast<const E*>(dy), static_cast<const E*>(sv), static_cast<const E*>(w), eps, T, H,
-                      static_cast<const E*>(dstream), static_cast<E*>(dx), parts);
-  };
-  switch (rs.nv) {
-    case 1: return go(norm::rmsnorm_backward_kernel<E, VEC, 1>);
-    case 2: return go(norm::rmsnorm_backward_kernel<E, VEC, 2>);
-    case 4: return go(norm::rmsnorm_backward_kernel<E, VEC, 4>);
-    default: break;
-  }
-  if constexpr (VEC == 1) {
-    if (rs.nv == 8) return go(norm::rmsnorm_backward_kernel<E, 1, 8>);
-    if (rs.nv == 16) return go(norm::rmsnorm_backward_kernel<E, 1, 16>);
-    if (rs.nv == 32) return go(norm::rmsnorm_backward_kernel<E, 1, 32>);
-  }
-  return fail(MOE_ERR_INVALID_ARG, "H=%d", H);
+  return with_row_shape<VEC>(rs, [&](auto nv, auto maxt) {
+    return launch_pdl("rmsnorm_backward_kernel launch",
+                      norm::rmsnorm_backward_kernel<E, VEC, decltype(nv)::value, decltype(maxt)::value>,
+                      dim3(blocks), dim3(rs.threads), 0, s, static_cast<const E*>(dy), static_cast<const E*>(sv),
+                      static_cast<const E*>(w), eps, T, H, static_cast<const E*>(dstream), static_cast<E*>(dx),
+                      parts);
+  });
 }
 
-int norm_parts(int64_t T) { return static_cast<int>(std::min<int64_t>(T, norm::kMaxParts)); }
+// Blocks of the backward pass, each with a row of dw partial sums: as many as
+// run at once on 148 SMs.
+int norm_parts(int64_t T, int64_t H) {
+  const int vec = H % 8 == 0 ? 8 : 1;
+  const RowShape rs = row_shape(H / vec);
+  const int maxt = rs.threads <= 256 && rs.nv <= 4 ? 256 : 1024;
+  const int per_sm = norm::backward_blocks(vec, rs.nv, maxt) * std::max(1, maxt / rs.threads);
+  return static_cast<int>(std::min<int64_t>(T, 148 * per_sm));
+}
 
 int check_norm_H(int64_t H) {
   REQUIRE(H >= 1 && H <= norm::kMaxH, "H=%lld outside [1, %d]", static_cast<long long>(H), norm::kMaxH);
@@ -133,20 +138,16 @@ struct Product {
   int nprob = 1, nseg = 1;
   int type = dense::kBF16;  // operand type, or kF32 outputs of int8
   const void* residual = nullptr;
-  void* saved = nullptr;     // three planes of M*N words (kGated: out, kDGate: in)
+  void* saved = nullptr;     // pre-activations (kGated: out, kDGate: in)
   void* out2 = nullptr;
   const float *a_scale = nullptr, *b_scale = nullptr, *bias = nullptr;
 };
 
 template <typename A>
-void common_args(A* g, const Product& p, int64_t M, int64_t N) {
+void common_args(A* g, const Product& p) {
   g->type = p.type;
   g->residual = static_cast<const uint16_t*>(p.residual);
-  uint16_t* s = static_cast<uint16_t*>(p.saved);
-  if (s != nullptr) {
-    g->saved = {s, s + M * N, s + 2 * M * N};
-    g->in = {s, s + M * N, s + 2 * M * N};
-  }
+  g->saved = static_cast<uint8_t*>(p.saved);
   g->out2 = p.out2;
   g->a_scale = p.a_scale;
   g->b_scale = p.b_scale;
@@ -197,7 +198,7 @@ int launch_pair(const Product& p, int sms, cudaStream_t s) {
     g.vec = g.vec && (q.N * (p.type == dense::kF32 ? 4 : 2)) % 16 == 0;
   }
   g.tiles = static_cast<int>(tiles);
-  common_args(&g, p, g.p[0].M, g.p[0].N);
+  common_args(&g, p);
   g.idesc = dense::make_idesc(KIND, p.type, A_MN, B_MN, dense::kBM, bn);
   const unsigned grid = 2 * static_cast<unsigned>(std::min<int64_t>(tiles, sms / 2));
   const size_t smem = bn == 256 ? dense::PairCfg<256>::SMEM : dense::PairCfg<128>::SMEM;
@@ -229,7 +230,7 @@ int launch_small_nt(const Product& p, int sms, cudaStream_t s) {
   g.split = 1;
   while (g.split < 8 && tiles * g.split * 2 <= 2 * sms && g.kblocks * g.nseg >= g.split * 4) g.split *= 2;
   g.out = p.out[0];
-  common_args(&g, p, g.T, g.N);
+  common_args(&g, p);
   g.idesc = dense::make_idesc(KIND, p.type, W_MN, false, dense::kSmallRows, NT);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(tiles * g.split));
@@ -344,7 +345,7 @@ int moe_add_rmsnorm(const void* x, const void* residual, const void* weight, flo
 
 size_t moe_add_rmsnorm_backward_workspace_bytes(int64_t T, int64_t H) {
   if (T < 0 || T > kMaxTokens || H < 1 || H > norm::kMaxH) return 0;
-  return static_cast<size_t>(norm_parts(T)) * static_cast<size_t>(H) * sizeof(float);
+  return static_cast<size_t>(norm_parts(T, H)) * static_cast<size_t>(H) * sizeof(float);
 }
 
 int moe_add_rmsnorm_backward(const void* dy, const void* s, const void* weight, float eps, int64_t T,
@@ -372,7 +373,7 @@ int moe_add_rmsnorm_backward(const void* dy, const void* s, const void* weight, 
     return MOE_OK;
   }
   float* parts = dweight ? static_cast<float*>(workspace) : nullptr;
-  const int blocks = norm_parts(T), h = static_cast<int>(H);
+  const int blocks = norm_parts(T, H), h = static_cast<int>(H);
   if (dtype == MOE_TYPE_BF16)
     rc = h % 8 == 0 ? launch_norm_bwd<__nv_bfloat16, 8>(T, dy, s, weight, eps, h, dstream, dx, parts, blocks, st)
                     : launch_norm_bwd<__nv_bfloat16, 1>(T, dy, s, weight, eps, h, dstream, dx, parts, blocks, st);
@@ -380,7 +381,7 @@ int moe_add_rmsnorm_backward(const void* dy, const void* s, const void* weight, 
     rc = h % 8 == 0 ? launch_norm_bwd<__half, 8>(T, dy, s, weight, eps, h, dstream, dx, parts, blocks, st)
                     : launch_norm_bwd<__half, 1>(T, dy, s, weight, eps, h, dstream, dx, parts, blocks, st);
   if (rc || !dweight) return rc;
-  return launch_pdl("rmsnorm_dw_kernel launch", norm::rmsnorm_dw_kernel, dim3((h + 31) / 32), dim3(256), 0, st,
+  return launch_pdl("rmsnorm_dw_kernel launch", norm::rmsnorm_dw_kernel, dim3((h + 31) / 32), dim3(1024), 0, st,
                     static_cast<const float*>(parts), blocks, h, dweight);
 }
 
@@ -415,7 +416,7 @@ int moe_int8_matmul(const int8_t* a, const float* a_scale, const int8_t* b, cons
 
 size_t moe_gated_ffn_saved_bytes(int64_t T, int64_t I) {
   if (T < 0 || T > kMaxTokens || I < 0 || I > kMaxDim) return 0;
-  return static_cast<size_t>(T) * static_cast<size_t>(I) * 6;
+  return static_cast<size_t>(dense::saved_bytes(T, I));
 }
 
 int moe_gated_ffn(const void* x, const void* w_gate, const void* w_up, const void* w_down, int64_t T,

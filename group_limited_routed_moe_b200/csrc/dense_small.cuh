@@ -46,8 +46,7 @@ struct SmallArgs {
   uint32_t idesc;
   void* out;
   const uint16_t* residual;
-  Saved saved;
-  SavedIn in;
+  uint8_t* saved;
   void* out2;
   const float *a_scale, *b_scale, *bias;
   uint64_t timeout_ns;
@@ -192,11 +191,13 @@ __global__ void __launch_bounds__(kSmallThreads)
     const int64_t at = (t0 + tok) * g.N + col;
     if constexpr (EPI == kGated) {
       const float gg = total(tok * kSmallRows + r), uu = total(tok * kSmallRows + 64 + r);
-      if (g.saved.g != nullptr) {
+      if (g.saved != nullptr) {
         const uint32_t gb = __float_as_uint(gg), ub = __float_as_uint(uu);
-        g.saved.g[at] = static_cast<uint16_t>(gb >> 16);
-        g.saved.u[at] = static_cast<uint16_t>(ub >> 16);
-        g.saved.lo[at] = static_cast<uint16_t>(((gb >> 8) & 0xFFu) | (ub & 0xFF00u));
+        uint8_t* sv = g.saved + saved_block(t0 + tok, col, g.N) + saved_word(t0 + tok, col);
+        *reinterpret_cast<uint16_t*>(sv) = static_cast<uint16_t>(gb >> 16);
+        *reinterpret_cast<uint16_t*>(sv + kSavedPlane) = static_cast<uint16_t>(ub >> 16);
+        *reinterpret_cast<uint16_t*>(sv + 2 * kSavedPlane) =
+            static_cast<uint16_t>(((gb >> 8) & 0xFFu) | (ub & 0xFF00u));
       }
       static_cast<uint16_t*>(g.out)[at] = pack1(silu(gg) * uu, g.type);
     } else {
@@ -205,15 +206,17 @@ __global__ void __launch_bounds__(kSmallThreads)
         if (g.residual != nullptr) v += unpack1(g.residual[at], g.type);
         static_cast<uint16_t*>(g.out)[at] = pack1(v, g.type);
       } else if constexpr (EPI == kDGate) {
-        const uint32_t l = g.in.lo[at];
-        const float gg = __uint_as_float((uint32_t(g.in.g[at]) << 16) | ((l & 0xFFu) << 8));
-        const float uu = __uint_as_float((uint32_t(g.in.u[at]) << 16) | (l & 0xFF00u));
-        const float sg = sigmoid(gg), act = silu(gg);
-        static_cast<uint16_t*>(g.out)[at] = pack1(v * uu * (sg + act * (1.f - sg)), g.type);
-        static_cast<uint16_t*>(g.out2)[at] = pack1(v * act, g.type);
+        const uint8_t* sv = g.saved + saved_block(t0 + tok, col, g.N) + saved_word(t0 + tok, col);
+        const uint32_t l = *reinterpret_cast<const uint16_t*>(sv + 2 * kSavedPlane);
+        const float gg = __uint_as_float((uint32_t(*reinterpret_cast<const uint16_t*>(sv)) << 16) | ((l & 0xFFu) << 8));
+        const float uu = __uint_as_float((uint32_t(*reinterpret_cast<const uint16_t*>(sv + kSavedPlane)) << 16) |
+                                         (l & 0xFF00u));
+        float dg, du;
+        dgate(v, gg, uu, dg, du);
+        static_cast<uint16_t*>(g.out)[at] = pack1(dg, g.type);
+        static_cast<uint16_t*>(g.out2)[at] = pack1(du, g.type);
       } else {
-        v = v * g.a_scale[t0 + tok] * g.b_scale[col];
-        if (g.bias != nullptr) v += g.bias[col];
+        v = fmaf(v * g.a_scale[t0 + tok], g.b_scale[col], g.bias != nullptr ? g.bias[col] : 0.f);
         if (g.type == kF32)
           static_cast<float*>(g.out)[at] = v;
         else

@@ -24,7 +24,6 @@ namespace moe {
 namespace norm {
 
 constexpr int kMaxH = 32768;       // a row lives in one block's registers
-constexpr int kMaxParts = 592;     // rows of dw partial sums (4 blocks on each of 148 SMs)
 constexpr int kGroup = 128;        // columns per scale in the grouped form
 
 enum Format { kSame = 0, kInt8 = 1, kE4m3 = 2 };
@@ -68,6 +67,27 @@ __device__ __forceinline__ float block_reduce(float v, float* red) {
   return r;
 }
 
+// Two sums at once.
+__device__ __forceinline__ void block_sum2(float& a, float& b, float (&red)[2][32]) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    a += __shfl_xor_sync(0xFFFFFFFFu, a, o);
+    b += __shfl_xor_sync(0xFFFFFFFFu, b, o);
+  }
+  if (blockDim.x == 32) return;
+  if ((threadIdx.x & 31) == 0) {
+    red[0][threadIdx.x >> 5] = a;
+    red[1][threadIdx.x >> 5] = b;
+  }
+  __syncthreads();
+  a = red[0][0];
+  b = red[1][0];
+  for (int w = 1; w < static_cast<int>(blockDim.x >> 5); ++w) {
+    a += red[0][w];
+    b += red[1][w];
+  }
+}
+
 __device__ __forceinline__ float scale_of(float amax, float top) {
   return max_nan(__fdiv_rn(amax, top), 1.17549435e-38f);
 }
@@ -97,8 +117,8 @@ __device__ __forceinline__ float row_scale(float amax, float eps) {
 
 // One row per block; a thread holds NV packs of VEC elements, pack i at column
 // (i * blockDim.x + threadIdx.x) * VEC.  group: 0 (a scale per row) or kGroup.
-template <typename E, int VEC, int NV, int FMT>
-__global__ void __launch_bounds__(1024)
+template <typename E, int VEC, int NV, int FMT, int MAXT>
+__global__ void __launch_bounds__(MAXT)
     add_rmsnorm_kernel(const E* x, const E* res, const E* __restrict__ w, float eps, int H,
                        int group, E* s_out, void* __restrict__ out, float* __restrict__ scales) {
   __shared__ float red[3][32];
@@ -236,10 +256,19 @@ __global__ void __launch_bounds__(1024)
   }
 }
 
-// Rows blockIdx.x, blockIdx.x + gridDim.x, ... ; dw partial sums of a block's
-// rows stay in registers and go to parts[blockIdx.x].
-template <typename E, int VEC, int NV>
-__global__ void __launch_bounds__(1024)
+// Blocks of the backward kernel that an SM runs at once, by the registers of a
+// thread's packs.
+__host__ __device__ constexpr int backward_blocks(int vec, int nv, int maxt) {
+  return maxt > 256 || vec * nv > 16 ? 1 : vec * nv > 8 ? 2 : 3;
+}
+
+// Rows blockIdx.x, blockIdx.x + gridDim.x, ...; the next row's loads are under
+// way while a row is summed and written (unless a block of 1024 threads has no
+// registers for it), since a block waits for its slowest warp in every row.
+// dw partial sums of a block's rows stay in registers and go to
+// parts[blockIdx.x].
+template <typename E, int VEC, int NV, int MAXT>
+__global__ void __launch_bounds__(MAXT, backward_blocks(VEC, NV, MAXT))
     rmsnorm_backward_kernel(const E* __restrict__ dy, const E* __restrict__ s,
                             const E* __restrict__ w, float eps, int64_t T, int H,
                             const E* __restrict__ dstream, E* __restrict__ dx,
@@ -254,17 +283,38 @@ __global__ void __launch_bounds__(1024)
   for (int i = 0; i < NV; ++i)
 #pragma unroll
     for (int j = 0; j < VEC; ++j) dw[i][j] = 0.f;
+  constexpr bool AHEAD = MAXT <= 256;
+  P sn[NV], dn[NV], tn[NV];  // the next row of s, dy, dstream
+  auto fetch = [&](int64_t row) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int p = i * blockDim.x + threadIdx.x;
+      if (p < nvec) {
+        const int64_t at = row * H + static_cast<int64_t>(p) * VEC;
+        sn[i] = *reinterpret_cast<const P*>(s + at);
+        dn[i] = *reinterpret_cast<const P*>(dy + at);
+        if (AHEAD && dstream != nullptr) tn[i] = *reinterpret_cast<const P*>(dstream + at);
+      }
+    }
+  };
+  if (AHEAD && blockIdx.x < T) fetch(blockIdx.x);
   int flip = 0;
   for (int64_t row = blockIdx.x; row < T; row += gridDim.x, flip ^= 1) {
     const int64_t base = row * H;
-    P sv[NV], dv[NV];
+    P sv[NV], dv[NV], tv[NV];
+    if (!AHEAD) fetch(row);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      sv[i] = sn[i];
+      dv[i] = dn[i];
+      tv[i] = tn[i];
+    }
+    if (AHEAD && row + gridDim.x < T) fetch(row + gridDim.x);
     float ss = 0.f, sd = 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int p = i * blockDim.x + threadIdx.x;
       if (p < nvec) {
-        sv[i] = *reinterpret_cast<const P*>(s + base + static_cast<int64_t>(p) * VEC);
-        dv[i] = *reinterpret_cast<const P*>(dy + base + static_cast<int64_t>(p) * VEC);
         P wv;
         if (w != nullptr) wv = *reinterpret_cast<const P*>(w + static_cast<int64_t>(p) * VEC);
 #pragma unroll
@@ -277,10 +327,10 @@ __global__ void __launch_bounds__(1024)
     }
     // the two sums use other words in every second row, so that a fast warp's
     // next row does not overwrite what a slow one still reads
-    ss = block_reduce<false>(ss, red[flip][0]);
-    sd = block_reduce<false>(sd, red[flip][1]);
-    float mult = 1.f, amax = 0.f;
+    block_sum2(ss, sd, red[flip]);
+    float mult = 1.f;
     if (out_of_range(ss)) {  // the whole block: as in the forward pass
+      float amax = 0.f;
 #pragma unroll
       for (int i = 0; i < NV; ++i)
         if (i * static_cast<int>(blockDim.x) + static_cast<int>(threadIdx.x) < nvec)
@@ -302,8 +352,7 @@ __global__ void __launch_bounds__(1024)
         }
       }
       __syncthreads();  // every thread has read the first sums
-      ss = block_reduce<false>(ss, red[flip][0]);
-      sd = block_reduce<false>(sd, red[flip][1]);
+      block_sum2(ss, sd, red[flip]);
     }
     const float rstd = rsqrtf(ss / static_cast<float>(H) + eps * mult * mult);  // of s * mult
     const float m = sd * rstd / static_cast<float>(H);                          // mean(dn n)
@@ -311,16 +360,16 @@ __global__ void __launch_bounds__(1024)
     for (int i = 0; i < NV; ++i) {
       const int p = i * blockDim.x + threadIdx.x;
       if (p < nvec) {
-        P wv, ds, o;
+        P wv, o;
         if (w != nullptr) wv = *reinterpret_cast<const P*>(w + static_cast<int64_t>(p) * VEC);
-        if (dstream != nullptr)
-          ds = *reinterpret_cast<const P*>(dstream + base + static_cast<int64_t>(p) * VEC);
+        if (!AHEAD && dstream != nullptr)
+          tv[i] = *reinterpret_cast<const P*>(dstream + base + static_cast<int64_t>(p) * VEC);
 #pragma unroll
         for (int j = 0; j < VEC; ++j) {
           const float n = to_f32(sv[i].e[j]) * mult * rstd, d = to_f32(dv[i].e[j]);
           dw[i][j] += d * n;
           float r = rstd * mult * (d * (w != nullptr ? to_f32(wv.e[j]) : 1.f) - n * m);
-          if (dstream != nullptr) r += to_f32(ds.e[j]);
+          if (dstream != nullptr) r += to_f32(tv[i].e[j]);
           o.e[j] = from_f32<E>(r);
         }
         *reinterpret_cast<P*>(dx + base + static_cast<int64_t>(p) * VEC) = o;
@@ -340,24 +389,26 @@ __global__ void __launch_bounds__(1024)
   }
 }
 
-// dw[c] = sum of parts[0..n)[c], in a fixed order: 32 columns per block, every
-// warp takes each 8th row, then the 8 warps' sums are added.
-__global__ void __launch_bounds__(256)
+// dw[c] = sum of parts[0..n)[c], in a fixed order: 32 columns per block, each
+// of 32 warps adds every 32nd row, then the warps' sums are added.
+__global__ void __launch_bounds__(1024)
     rmsnorm_dw_kernel(const float* __restrict__ parts, int n, int H, float* __restrict__ dw) {
-  __shared__ float sum[8][32];
+  __shared__ float sum[32][33];
   griddep_wait();
   griddep_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int c = blockIdx.x * 32 + lane;
   float a = 0.f;
-  if (c < H)
-    for (int r = warp; r < n; r += 8) a += parts[static_cast<int64_t>(r) * H + c];
+  if (c < H) {
+#pragma unroll 8
+    for (int r = warp; r < n; r += 32) a += parts[static_cast<int64_t>(r) * H + c];
+  }
   sum[warp][lane] = a;
   __syncthreads();
-  if (warp == 0 && c < H) {
-    for (int i = 1; i < 8; ++i) a += sum[i][lane];
-    dw[c] = a;
-  }
+  a = sum[lane][warp];  // column `warp` of the block, row sums across the lanes
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) a += __shfl_xor_sync(0xFFFFFFFFu, a, o);
+  if (lane == 0 && blockIdx.x * 32 + warp < H) dw[blockIdx.x * 32 + warp] = a;
 }
 
 }  // namespace norm

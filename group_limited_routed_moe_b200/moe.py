@@ -780,10 +780,11 @@ NORM_GROUP = 128
 
 
 def _expect(name: str, t: torch.Tensor, shape, dtype, device) -> None:
-    if not isinstance(t, torch.Tensor) or t.dtype != dtype or tuple(t.shape) != tuple(shape) \
-            or not t.is_contiguous() or t.device != device:
-        got = f"{t.dtype} {tuple(t.shape)} on {t.device}" if isinstance(t, torch.Tensor) else repr(t)
-        raise ValueError(f"{name}: expected contiguous {dtype} {tuple(shape)} on {device}, got {got}")
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == device \
+            and t.is_contiguous():
+        return
+    got = f"{t.dtype} {tuple(t.shape)} on {t.device}" if isinstance(t, torch.Tensor) else repr(t)
+    raise ValueError(f"{name}: expected contiguous {dtype} {tuple(shape)} on {device}, got {got}")
 
 
 def _leading(name: str, t: torch.Tensor, dtypes) -> tuple[torch.device, torch.dtype]:
@@ -796,23 +797,32 @@ def _leading(name: str, t: torch.Tensor, dtypes) -> tuple[torch.device, torch.dt
 
 class _on:
     """Makes a tensor's device current, and on it the stream of the call, so
-    that what the call allocates belongs to that stream."""
+    that what the call allocates belongs to that stream; enters with the raw
+    stream.  On the current device and stream, nothing has to be set."""
+
+    __slots__ = ("device", "stream", "guards")
 
     def __init__(self, device, stream):
-        self.device = torch.cuda.device(device)
-        self.stream = stream
+        self.device, self.stream, self.guards = device, stream, ()
 
     def __enter__(self):
-        self.device.__enter__()
-        self.use = torch.cuda.stream(self.stream) if self.stream is not None else None
-        if self.use is not None:
-            self.use.__enter__()
-        return _stream()
+        if self.stream is not None:
+            if self.stream.device != self.device:
+                raise ValueError(f"stream on {self.stream.device}, tensors on {self.device}")
+            self.guards = (torch.cuda.stream(self.stream),)
+        elif torch.cuda.current_device() != self.device.index:
+            self.guards = (torch.cuda.device(self.device),)
+        for g in self.guards:
+            g.__enter__()
+        return torch._C._cuda_getCurrentRawStream(self.device.index)
 
     def __exit__(self, *exc):
-        if self.use is not None:
-            self.use.__exit__(*exc)
-        self.device.__exit__(*exc)
+        for g in self.guards:
+            g.__exit__(*exc)
+
+
+def _adr(t):
+    return None if t is None else t.data_ptr()
 
 
 def _new(name, t, shape, dtype, device):
@@ -822,17 +832,27 @@ def _new(name, t, shape, dtype, device):
     return t
 
 
+def _new_like(name, t, like):
+    if t is None:
+        return torch.empty_like(like)
+    _expect(name, t, like.shape, like.dtype, like.device)
+    return t
+
+
 def _scratch(name: str, t, nbytes: int, device):
     """A workspace of at least nbytes bytes (any type), or a fresh one."""
     if t is None:
         return torch.empty(nbytes, dtype=torch.uint8, device=device)
-    if not t.is_cuda or t.device != device or not t.is_contiguous():
+    if not isinstance(t, torch.Tensor) or t.device != device or not t.is_contiguous():
         raise ValueError(f"{name}: expected contiguous memory on {device}")
     return t
 
 
 def _nbytes(t) -> int:
     return 0 if t is None else t.numel() * t.element_size()
+
+
+_T16 = (torch.bfloat16, torch.float16)
 
 
 def moe_add_rmsnorm(x: torch.Tensor, residual: torch.Tensor | None = None, weight=None, eps: float = 1e-6,
@@ -842,7 +862,7 @@ def moe_add_rmsnorm(x: torch.Tensor, residual: torch.Tensor | None = None, weigh
     include/moe.h).  Returns (s, out, scales): out in x's type ("same"; scales
     None), int8 or float8_e4m3fn; scales fp32 [T, 1], or [T, ceil(H / 128)]
     with group = 128.  Without residual s is x."""
-    dev, dt = _leading("x", x, (torch.bfloat16, torch.float16))
+    dev, dt = _leading("x", x, _T16)
     if out_format not in NORM_FORMATS:
         raise ValueError(f"out_format {out_format!r}: one of {sorted(NORM_FORMATS)}")
     fmt = NORM_FORMATS[out_format]
@@ -857,15 +877,16 @@ def moe_add_rmsnorm(x: torch.Tensor, residual: torch.Tensor | None = None, weigh
         if residual is None:
             stream_out = x
         else:
-            stream_out = _new("stream_out", stream_out, x.shape, dt, dev)
-        out = _new("out", out, x.shape, (dt, torch.int8, torch.float8_e4m3fn)[fmt], dev)
+            stream_out = _new_like("stream_out", stream_out, x)
         if fmt:
+            out = _new("out", out, x.shape, torch.int8 if fmt == 1 else torch.float8_e4m3fn, dev)
             scales = _new("scales", scales, (T, -(-H // group) if group else 1), torch.float32, dev)
         else:
+            out = _new_like("out", out, x)
             scales = None
         _check("moe_add_rmsnorm", lib.moe_add_rmsnorm(
-            _ptr(x), _ptr(residual), _ptr(weight), eps, T, H, _TYPES[dt],
-            None if residual is None else _ptr(stream_out), fmt, group, _ptr(out), _ptr(scales), s))
+            _adr(x), _adr(residual), _adr(weight), eps, T, H, _TYPES[dt],
+            None if residual is None else _adr(stream_out), fmt, group, _adr(out), _adr(scales), s))
     return stream_out, out, scales
 
 
@@ -873,7 +894,7 @@ def moe_add_rmsnorm_backward(dy: torch.Tensor, s: torch.Tensor, weight=None, eps
                              dx=None, dweight=None, need_dweight: bool = True, workspace=None, stream=None):
     """Gradients of moe_add_rmsnorm's 16-bit form: (dx [T, H], dweight [H] fp32
     or None); dx is the gradient of x and of residual (see include/moe.h)."""
-    dev, dt = _leading("dy", dy, (torch.bfloat16, torch.float16))
+    dev, dt = _leading("dy", dy, _T16)
     T, H = dy.shape
     _expect("s", s, dy.shape, dt, dev)
     if weight is not None:
@@ -881,7 +902,7 @@ def moe_add_rmsnorm_backward(dy: torch.Tensor, s: torch.Tensor, weight=None, eps
     if dstream is not None:
         _expect("dstream", dstream, dy.shape, dt, dev)
     with _on(dev, stream) as st:
-        dx = _new("dx", dx, dy.shape, dt, dev)
+        dx = _new_like("dx", dx, dy)
         if need_dweight:
             dweight = _new("dweight", dweight, (H,), torch.float32, dev)
             workspace = _scratch("workspace", workspace,
@@ -889,8 +910,8 @@ def moe_add_rmsnorm_backward(dy: torch.Tensor, s: torch.Tensor, weight=None, eps
         else:
             dweight = workspace = None
         _check("moe_add_rmsnorm_backward", lib.moe_add_rmsnorm_backward(
-            _ptr(dy), _ptr(s), _ptr(weight), eps, T, H, _TYPES[dt], _ptr(dstream), _ptr(dx), _ptr(dweight),
-            _ptr(workspace), _nbytes(workspace), st))
+            _adr(dy), _adr(s), _adr(weight), eps, T, H, _TYPES[dt], _adr(dstream), _adr(dx), _adr(dweight),
+            _adr(workspace), _nbytes(workspace), st))
     return dx, dweight
 
 
@@ -913,12 +934,12 @@ def moe_int8_matmul(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor, b_s
     with _on(dev, stream) as s:
         out = _new("out", out, (T, N), out_dtype, dev)
         _check("moe_int8_matmul", lib.moe_int8_matmul(
-            _ptr(a), _ptr(a_scale), _ptr(b), _ptr(b_scale), _ptr(bias), T, N, K, _TYPES[out_dtype], _ptr(out), s))
+            _adr(a), _adr(a_scale), _adr(b), _adr(b_scale), _adr(bias), T, N, K, _TYPES[out_dtype], _adr(out), s))
     return out
 
 
 def _ffn_shapes(x, w_gate, w_up, w_down):
-    dev, dt = _leading("x", x, (torch.bfloat16, torch.float16))
+    dev, dt = _leading("x", x, _T16)
     T, H = x.shape
     if not isinstance(w_gate, torch.Tensor) or w_gate.dim() != 2:
         raise ValueError("w_gate: expected a matrix [H, I]")
@@ -939,11 +960,11 @@ def moe_gated_ffn(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, w_d
         _expect("residual", residual, (T, H), dt, dev)
     with _on(dev, stream) as s:
         h = _new("h", h, (T, I), dt, dev)
-        y = _new("y", y, (T, H), dt, dev)
+        y = _new_like("y", y, x)
         pre = torch.empty(int(lib.moe_gated_ffn_saved_bytes(T, I)), dtype=torch.uint8, device=dev) if save else None
         _check("moe_gated_ffn", lib.moe_gated_ffn(
-            _ptr(x), _ptr(w_gate), _ptr(w_up), _ptr(w_down), T, H, I, _TYPES[dt], _ptr(residual), _ptr(h),
-            _ptr(pre), _ptr(y), s))
+            _adr(x), _adr(w_gate), _adr(w_up), _adr(w_down), T, H, I, _TYPES[dt], _adr(residual), _adr(h),
+            _adr(pre), _adr(y), s))
     return (y, (h, pre)) if save else y
 
 
@@ -969,8 +990,8 @@ def moe_gated_ffn_backward(dy: torch.Tensor, x: torch.Tensor, w_gate: torch.Tens
         else:
             workspace = None
         _check("moe_gated_ffn_backward", lib.moe_gated_ffn_backward(
-            _ptr(dy), _ptr(x), _ptr(w_gate), _ptr(w_up), _ptr(w_down), _ptr(h), _ptr(pre), T, H, I, _TYPES[dt],
-            *(_ptr(t) for t in outs), _ptr(workspace), _nbytes(workspace), s))
+            _adr(dy), _adr(x), _adr(w_gate), _adr(w_up), _adr(w_down), _adr(h), _adr(pre), T, H, I, _TYPES[dt],
+            *(_adr(t) for t in outs), _adr(workspace), _nbytes(workspace), s))
     return tuple(outs)
 
 
@@ -1009,9 +1030,9 @@ def moe_layer_normed(x: torch.Tensor, residual, norm_weight, eps: float, packed_
         if workspace is None:
             workspace = alloc_layer_normed_workspace(T, dev)
         _check("moe_layer_normed", lib.moe_layer_normed(
-            _ptr(x), _ptr(residual), _ptr(norm_weight), eps, _ptr(packed_router), _ptr(bias), _ptr(packed_w), T,
-            None if residual is None else _ptr(stream_out), _ptr(out), _ptr(topk_idx_out), _ptr(topk_w_out),
-            _ptr(workspace), _nbytes(workspace), s))
+            _adr(x), _adr(residual), _adr(norm_weight), eps, _adr(packed_router), _adr(bias), _adr(packed_w), T,
+            None if residual is None else _adr(stream_out), _adr(out), _adr(topk_idx_out), _adr(topk_w_out),
+            _adr(workspace), _nbytes(workspace), s))
     return stream_out, out
 
 

@@ -689,7 +689,8 @@ int moe_int8_matmul(const int8_t* a, const float* a_scale, const int8_t* b, cons
                     moe_stream_t stream);
 
 /* Bytes of the pre-activations moe_gated_ffn saves for its backward pass: the
- * upper 24 bits of the fp32 x W_gate and x W_up (6 T I bytes). */
+ * upper 24 bits of the fp32 x W_gate and x W_up, in blocks of 32 x 32 (6 bytes
+ * for each element of T and I rounded up to multiples of 32). */
 size_t moe_gated_ffn_saved_bytes(int64_t T, int64_t I);
 
 /* The gated feed-forward block of any width (the routed experts' FFN, dense):

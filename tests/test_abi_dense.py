@@ -53,7 +53,7 @@ def test_norm_backward_workspace():
     need = L.moe_add_rmsnorm_backward_workspace_bytes
     assert need(4, 64) == 4 * 64 * 4
     assert need(0, 64) == 0 and need(-1, 64) == 0 and need(4, 0) == 0 and need(4, 32769) == 0
-    assert need(1 << 22, 64) == need(1 << 12, 64) == 592 * 64 * 4
+    assert need(1 << 22, 64) == need(1 << 20, 64) < 4096 * 64 * 4  # rows of partial sums: bounded
     assert _norm_bwd(n=need(4, 64) - 1) == WS
     assert _norm_bwd(ws=None) == WS
     assert _norm_bwd(T=0, dw=None, dy=None, s=None, dx=None, ws=None) == OK
@@ -111,7 +111,7 @@ def test_ffn_backward_refusals(kw):
 
 
 def test_ffn_sizes_and_workspace():
-    assert L.moe_gated_ffn_saved_bytes(5, 64) == 5 * 64 * 6
+    assert L.moe_gated_ffn_saved_bytes(5, 72) == 32 * 96 * 6 and L.moe_gated_ffn_saved_bytes(64, 64) == 64 * 64 * 6
     assert L.moe_gated_ffn_backward_workspace_bytes(5, 64) == 5 * 64 * 4
     for f in (L.moe_gated_ffn_saved_bytes, L.moe_gated_ffn_backward_workspace_bytes):
         assert f(-1, 64) == 0 and f(5, -8) == 0 and f(5, 65544) == 0 and f((1 << 22) + 1, 64) == 0
