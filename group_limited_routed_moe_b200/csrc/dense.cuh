@@ -58,6 +58,17 @@ __device__ __forceinline__ int saved_word(int64_t row, int64_t col) {
   return static_cast<int>(((col & 31) >> 3) * 512 + (row & 31) * 16 + (col & 7) * 2);
 }
 
+// The low-plane words of two neighbouring columns (e, o) from the fp32 bits of g and u.
+__device__ __forceinline__ uint32_t saved_low(uint32_t ge, uint32_t ue, uint32_t go, uint32_t uo) {
+  return ((ge >> 8) & 0xFFu) | (ue & 0xFF00u) | ((go << 8) & 0xFF0000u) | ((uo << 16) & 0xFF000000u);
+}
+// g and u of column j (0, 1) of a pair of words.
+__device__ __forceinline__ void saved_get(uint32_t gh, uint32_t uh, uint32_t lo, int j, float& g, float& u) {
+  const uint32_t l = lo >> (16 * j);
+  g = __uint_as_float((j ? gh & 0xFFFF0000u : gh << 16) | ((l & 0xFFu) << 8));
+  u = __uint_as_float((j ? uh & 0xFFFF0000u : uh << 16) | (l & 0xFF00u));
+}
+
 struct Problem {
   int64_t M, N;   // rows and columns of the output
   int mt, nt;     // tiles
@@ -102,9 +113,12 @@ __device__ __forceinline__ uint32_t map_to_rank(uint32_t addr, uint32_t rank) {
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
-__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+__device__ __forceinline__ uint4 ld_cluster_v4(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared::cluster.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr)
+               : "memory");
   return v;
 }
 // TMA load into this CTA's shared memory that signals `bar` (a shared::cluster
@@ -516,16 +530,13 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
           if (g.saved != nullptr) {
             uint4* sv = reinterpret_cast<uint4*>(g.saved + saved_block(row0, col, P.N)) + lane;
             auto hi = [](uint32_t e, uint32_t o) { return (e >> 16) | (o & 0xFFFF0000u); };
-            auto mid = [](uint32_t ge, uint32_t ue, uint32_t go, uint32_t uo) {
-              return ((ge >> 8) & 0xFFu) | (ue & 0xFF00u) | ((go << 8) & 0xFF0000u) | ((uo << 16) & 0xFF000000u);
-            };
 #pragma unroll
             for (int q4 = 0; q4 < 4; ++q4) {
               const uint32_t *e = x + 8 * q4, *f = x1 + 8 * q4;
               sv[q4 * 32] = make_uint4(hi(e[0], e[1]), hi(e[2], e[3]), hi(e[4], e[5]), hi(e[6], e[7]));
               sv[(4 + q4) * 32] = make_uint4(hi(f[0], f[1]), hi(f[2], f[3]), hi(f[4], f[5]), hi(f[6], f[7]));
-              sv[(8 + q4) * 32] = make_uint4(mid(e[0], f[0], e[1], f[1]), mid(e[2], f[2], e[3], f[3]),
-                                             mid(e[4], f[4], e[5], f[5]), mid(e[6], f[6], e[7], f[7]));
+              sv[(8 + q4) * 32] = make_uint4(saved_low(e[0], f[0], e[1], f[1]), saved_low(e[2], f[2], e[3], f[3]),
+                                             saved_low(e[4], f[4], e[5], f[5]), saved_low(e[6], f[6], e[7], f[7]));
             }
           }
 #pragma unroll
@@ -555,9 +566,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
             float dg[2], du[2];
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-              const uint32_t l = lw >> (16 * j);
-              const float gg = __uint_as_float((j ? hw & 0xFFFF0000u : hw << 16) | ((l & 0xFFu) << 8));
-              const float uu = __uint_as_float((j ? uw & 0xFFFF0000u : uw << 16) | (l & 0xFF00u));
+              float gg, uu;
+              saved_get(hw, uw, lw, j, gg, uu);
               dgate(__uint_as_float(x[2 * i + j]), gg, uu, dg[j], du[j]);
             }
             pg[i] = pack2(dg[0], dg[1], g.type);

@@ -140,6 +140,7 @@ struct Product {
   const void* residual = nullptr;
   void* saved = nullptr;     // pre-activations (kGated: out, kDGate: in)
   void* out2 = nullptr;
+  bool early = false;        // follows a launch of the same call that does not write b
   const float *a_scale = nullptr, *b_scale = nullptr, *bias = nullptr;
 };
 
@@ -228,7 +229,8 @@ int launch_small_nt(const Product& p, int sms, cudaStream_t s) {
   // split k over the cluster until the CTAs fill the SMs twice, as long as
   // each keeps 2 k-blocks
   g.split = 1;
-  while (g.split < 8 && tiles * g.split * 2 <= 2 * sms && g.kblocks * g.nseg >= g.split * 4) g.split *= 2;
+  while (g.split < dense::kMaxSplit && tiles * g.split * 2 <= 2 * sms && g.kblocks * g.nseg >= g.split * 4) g.split *= 2;
+  g.early = p.early;
   g.out = p.out[0];
   common_args(&g, p);
   g.idesc = dense::make_idesc(KIND, p.type, W_MN, false, dense::kSmallRows, NT);
@@ -448,6 +450,7 @@ int moe_gated_ffn(const void* x, const void* w_gate, const void* w_up, const voi
   down.out[0] = y;
   down.type = dtype;
   down.residual = residual;
+  down.early = true;
   return launch_product<dense::kF16Kind, true, dense::kPlain>(down, sms, s);
 }
 
@@ -506,6 +509,7 @@ int moe_gated_ffn_backward(const void* dy, const void* x, const void* w_gate, co
     p.b[0] = {w_gate, H, I, false};
     p.b[1] = {w_up, H, I, false};
     p.nseg = 2;
+    p.early = true;
     p.out[0] = dx;
     p.type = dtype;
     rc = launch_product<dense::kF16Kind, false, dense::kPlain>(p, sms, s);

@@ -16,6 +16,7 @@ namespace moe {
 namespace dense {
 
 constexpr int kSmallThreads = 256;
+constexpr int kMaxSplit = 8;
 constexpr int kSmallRows = 128;  // weight rows of a tile (kGated: 64 gate and 64 up columns)
 
 template <int NT>
@@ -41,7 +42,8 @@ struct SmallArgs {
   int64_t T, N;            // tokens; weight columns (outputs per token)
   int wt;                  // weight tiles
   int nseg, kblocks;       // k segments, k-blocks of a segment
-  int split;               // CTAs of a cluster
+  int split;               // CTAs of a cluster, 1 .. kMaxSplit
+  bool early;              // the weights may be read before the preceding launch has finished
   int type;
   uint32_t idesc;
   void* out;
@@ -86,13 +88,35 @@ __global__ void __launch_bounds__(kSmallThreads)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = S->tmem_base;
-  griddep_wait();
-  griddep_launch_dependents();
 
   // this CTA's k-blocks: an even share of all segments' blocks
   const int kbs = g.kblocks * g.nseg;
   const int kb0 = static_cast<int>(int64_t(kbs) * rank / g.split);
   const int kb1 = static_cast<int>(int64_t(kbs) * (rank + 1) / g.split);
+
+  auto load_w = [&](int kb, int s) {  // k-block kb of the weights into stage s
+    const int seg = kb >= g.kblocks ? 1 : 0;
+    const int k0 = (kb - seg * g.kblocks) * KE;
+    const uint32_t sw = smem_u32(smem + s * C::STAGE);
+    mbar_arrive_expect_tx(&S->full[s], C::STAGE);
+    if constexpr (EPI == kGated) {
+      tma_load_2d(sw, &g.w[0], wtile * 64, k0, &S->full[s]);
+      tma_load_2d(sw + 8192, &g.w[1], wtile * 64, k0, &S->full[s]);
+    } else if constexpr (W_MN) {
+      tma_load_2d(sw, &g.w[seg], wtile * 128, k0, &S->full[s]);
+      tma_load_2d(sw + 8192, &g.w[seg], wtile * 128 + 64, k0, &S->full[s]);
+    } else {
+      tma_load_2d(sw, &g.w[seg], k0, wtile * 128, &S->full[s]);
+    }
+  };
+  // Where the launch before this one is a step of the same call (which waited
+  // for everything before it), the weights are no output of it: their first
+  // stages are read while it still runs.
+  int ahead = 0;
+  if (g.early && warp == 0 && lane == 0)
+    for (; ahead < C::STAGES && kb0 + ahead < kb1; ++ahead) load_w(kb0 + ahead, ahead);
+  griddep_wait();
+  griddep_launch_dependents();
 
   if (warp == 0) {
     if (lane == 0) {
@@ -106,18 +130,8 @@ __global__ void __launch_bounds__(kSmallThreads)
         }
         const int seg = kb >= g.kblocks ? 1 : 0;
         const int k0 = (kb - seg * g.kblocks) * KE;
-        const uint32_t sw = smem_u32(smem + s * C::STAGE), sx = sw + kSmallRows * kKB;
-        mbar_arrive_expect_tx(&S->full[s], C::STAGE);
-        if constexpr (EPI == kGated) {
-          tma_load_2d(sw, &g.w[0], wtile * 64, k0, &S->full[s]);
-          tma_load_2d(sw + 8192, &g.w[1], wtile * 64, k0, &S->full[s]);
-        } else if constexpr (W_MN) {
-          tma_load_2d(sw, &g.w[seg], wtile * 128, k0, &S->full[s]);
-          tma_load_2d(sw + 8192, &g.w[seg], wtile * 128 + 64, k0, &S->full[s]);
-        } else {
-          tma_load_2d(sw, &g.w[seg], k0, wtile * 128, &S->full[s]);
-        }
-        tma_load_2d(sx, &g.x[seg], k0, ttile * NT, &S->full[s]);
+        if (it >= ahead) load_w(kb, s);
+        tma_load_2d(smem_u32(smem + s * C::STAGE) + kSmallRows * kKB, &g.x[seg], k0, ttile * NT, &S->full[s]);
       }
       if (!ok)  // let the copies already issued land before the block can exit
         for (int i = max(0, it - C::STAGES); i < it; ++i)
@@ -167,61 +181,97 @@ __global__ void __launch_bounds__(kSmallThreads)
   tc_fence_before();
   if (g.split > 1) cluster_sync(); else __syncthreads();
 
-  // a share of the outputs: element e is token e / PER, weight row e % PER
-  constexpr int PER = EPI == kGated ? 64 : kSmallRows;
+  // A share of the outputs: unit e is 4 consecutive weight rows of a token.  All
+  // ranks' parts of a unit are loaded before they are added up (one after the
+  // other, each load from another SM's memory would cost its full latency).
+  constexpr int PER = EPI == kGated ? 64 : kSmallRows, UNITS = PER / 4;
   const int64_t t0 = int64_t(ttile) * NT;
   const int ntok = static_cast<int>(min(int64_t(NT), g.T - t0));
   const uint32_t mine = smem_u32(part);
-  auto total = [&](int index) {  // sum over the ranks, in rank order
+  auto total = [&](int index, float (&sum)[4]) {  // sums over the ranks, in rank order
+    uint4 v[kMaxSplit];
+#pragma unroll
+    for (int r = 0; r < kMaxSplit; ++r)
+      if (r < g.split) v[r] = ld_cluster_v4(map_to_rank(mine + index * 4, r));
     if constexpr (KIND == kI8Kind) {
-      int a = 0;
-      for (int r = 0; r < g.split; ++r)
-        a += __float_as_int(ld_cluster_f32(map_to_rank(mine + index * 4, r)));
-      return static_cast<float>(a);
+      int a[4] = {0, 0, 0, 0};
+#pragma unroll
+      for (int r = 0; r < kMaxSplit; ++r)
+        if (r < g.split) {
+          a[0] += int(v[r].x); a[1] += int(v[r].y); a[2] += int(v[r].z); a[3] += int(v[r].w);
+        }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) sum[i] = static_cast<float>(a[i]);
     } else {
-      float a = 0.f;
-      for (int r = 0; r < g.split; ++r) a += ld_cluster_f32(map_to_rank(mine + index * 4, r));
-      return a;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) sum[i] = 0.f;
+#pragma unroll
+      for (int r = 0; r < kMaxSplit; ++r)
+        if (r < g.split) {
+          sum[0] += __uint_as_float(v[r].x); sum[1] += __uint_as_float(v[r].y);
+          sum[2] += __uint_as_float(v[r].z); sum[3] += __uint_as_float(v[r].w);
+        }
     }
   };
-  for (int e = rank * kSmallThreads + threadIdx.x; e < ntok * PER; e += g.split * kSmallThreads) {
-    const int tok = e / PER, r = e % PER;
-    const int64_t col = int64_t(wtile) * PER + r;
+  for (int e = rank * kSmallThreads + threadIdx.x; e < ntok * UNITS; e += g.split * kSmallThreads) {
+    const int tok = e / UNITS, r = e % UNITS * 4;
+    const int64_t col = int64_t(wtile) * PER + r, row = t0 + tok;
     if (col >= g.N) continue;
-    const int64_t at = (t0 + tok) * g.N + col;
-    if constexpr (EPI == kGated) {
-      const float gg = total(tok * kSmallRows + r), uu = total(tok * kSmallRows + 64 + r);
-      if (g.saved != nullptr) {
-        const uint32_t gb = __float_as_uint(gg), ub = __float_as_uint(uu);
-        uint8_t* sv = g.saved + saved_block(t0 + tok, col, g.N) + saved_word(t0 + tok, col);
-        *reinterpret_cast<uint16_t*>(sv) = static_cast<uint16_t>(gb >> 16);
-        *reinterpret_cast<uint16_t*>(sv + kSavedPlane) = static_cast<uint16_t>(ub >> 16);
-        *reinterpret_cast<uint16_t*>(sv + 2 * kSavedPlane) =
-            static_cast<uint16_t>(((gb >> 8) & 0xFFu) | (ub & 0xFF00u));
-      }
-      static_cast<uint16_t*>(g.out)[at] = pack1(silu(gg) * uu, g.type);
-    } else {
-      float v = total(tok * kSmallRows + r);
-      if constexpr (EPI == kPlain) {
-        if (g.residual != nullptr) v += unpack1(g.residual[at], g.type);
-        static_cast<uint16_t*>(g.out)[at] = pack1(v, g.type);
-      } else if constexpr (EPI == kDGate) {
-        const uint8_t* sv = g.saved + saved_block(t0 + tok, col, g.N) + saved_word(t0 + tok, col);
-        const uint32_t l = *reinterpret_cast<const uint16_t*>(sv + 2 * kSavedPlane);
-        const float gg = __uint_as_float((uint32_t(*reinterpret_cast<const uint16_t*>(sv)) << 16) | ((l & 0xFFu) << 8));
-        const float uu = __uint_as_float((uint32_t(*reinterpret_cast<const uint16_t*>(sv + kSavedPlane)) << 16) |
-                                         (l & 0xFF00u));
-        float dg, du;
-        dgate(v, gg, uu, dg, du);
-        static_cast<uint16_t*>(g.out)[at] = pack1(dg, g.type);
-        static_cast<uint16_t*>(g.out2)[at] = pack1(du, g.type);
-      } else {
-        v = fmaf(v * g.a_scale[t0 + tok], g.b_scale[col], g.bias != nullptr ? g.bias[col] : 0.f);
+    const int64_t at = row * g.N + col;
+    float y[4], z[4];
+    total(tok * kSmallRows + r, y);
+    if constexpr (EPI == kScaled) {
+      const float sa = g.a_scale[row];
+      // rows of any length: element by element
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (col + i >= g.N) break;
+        const float v = fmaf(y[i] * sa, g.b_scale[col + i], g.bias != nullptr ? g.bias[col + i] : 0.f);
         if (g.type == kF32)
-          static_cast<float*>(g.out)[at] = v;
+          static_cast<float*>(g.out)[at + i] = v;
         else
-          static_cast<uint16_t*>(g.out)[at] = pack1(v, g.type);
+          static_cast<uint16_t*>(g.out)[at + i] = pack1(v, g.type);
       }
+    } else {  // N is a multiple of 8
+      uint8_t* sv = nullptr;
+      if constexpr (EPI != kPlain)
+        if (g.saved != nullptr) sv = g.saved + saved_block(row, col, g.N) + saved_word(row, col);
+      if constexpr (EPI == kGated) {
+        total(tok * kSmallRows + 64 + r, z);
+        if (sv != nullptr) {
+          uint32_t w[4], l[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            w[i] = __float_as_uint(y[i]);
+            l[i] = __float_as_uint(z[i]);
+          }
+          *reinterpret_cast<uint2*>(sv) = make_uint2((w[0] >> 16) | (w[1] & 0xFFFF0000u), (w[2] >> 16) | (w[3] & 0xFFFF0000u));
+          *reinterpret_cast<uint2*>(sv + kSavedPlane) =
+              make_uint2((l[0] >> 16) | (l[1] & 0xFFFF0000u), (l[2] >> 16) | (l[3] & 0xFFFF0000u));
+          *reinterpret_cast<uint2*>(sv + 2 * kSavedPlane) = make_uint2(saved_low(w[0], l[0], w[1], l[1]), saved_low(w[2], l[2], w[3], l[3]));
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y[i] = silu(y[i]) * z[i];
+      } else if constexpr (EPI == kPlain) {
+        if (g.residual != nullptr) {
+          const uint2 q = *reinterpret_cast<const uint2*>(g.residual + at);
+          y[0] += unpack_lo(q.x, g.type); y[1] += unpack_hi(q.x, g.type);
+          y[2] += unpack_lo(q.y, g.type); y[3] += unpack_hi(q.y, g.type);
+        }
+      } else {
+        const uint2 gh = *reinterpret_cast<const uint2*>(sv), uh = *reinterpret_cast<const uint2*>(sv + kSavedPlane),
+                    lo = *reinterpret_cast<const uint2*>(sv + 2 * kSavedPlane);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float gg, uu;
+          saved_get((&gh.x)[i / 2], (&uh.x)[i / 2], (&lo.x)[i / 2], i % 2, gg, uu);
+          dgate(y[i], gg, uu, y[i], z[i]);
+        }
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(g.out2) + at) =
+            make_uint2(pack2(z[0], z[1], g.type), pack2(z[2], z[3], g.type));
+      }
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(g.out) + at) =
+          make_uint2(pack2(y[0], y[1], g.type), pack2(y[2], y[3], g.type));
     }
   }
   // a peer may still read this CTA's partial sums

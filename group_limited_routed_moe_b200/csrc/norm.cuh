@@ -18,6 +18,8 @@
 #pragma once
 #include <cuda_fp8.h>
 
+#include <type_traits>
+
 #include "common.cuh"
 
 namespace moe {
@@ -28,12 +30,57 @@ constexpr int kGroup = 128;        // columns per scale in the grouped form
 
 enum Format { kSame = 0, kInt8 = 1, kE4m3 = 2 };
 
-template <typename E> __device__ __forceinline__ float to_f32(E v);
-template <> __device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
-template <> __device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
-template <typename E> __device__ __forceinline__ E from_f32(float v);
-template <> __device__ __forceinline__ __nv_bfloat16 from_f32(float v) { return __float2bfloat16_rn(v); }
-template <> __device__ __forceinline__ __half from_f32(float v) { return __float2half_rn(v); }
+// VEC consecutive 16-bit elements as they lie in memory, in whole registers:
+// 8 (16 bytes) or 1.  (An array of 16-bit members would take a register each.)
+template <typename E, int VEC>
+struct alignas(2 * VEC) Pack {
+  uint32_t w[VEC / 2];
+  __device__ __forceinline__ void get(float (&f)[VEC]) const {
+#pragma unroll
+    for (int i = 0; i < VEC / 2; ++i) {
+      if constexpr (std::is_same<E, __nv_bfloat16>::value) {
+        f[2 * i] = bf16_lo(w[i]);
+        f[2 * i + 1] = bf16_hi(w[i]);
+      } else {
+        const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+        f[2 * i] = v.x;
+        f[2 * i + 1] = v.y;
+      }
+    }
+  }
+  __device__ __forceinline__ void set(const float (&f)[VEC]) {
+#pragma unroll
+    for (int i = 0; i < VEC / 2; ++i) {
+      if constexpr (std::is_same<E, __nv_bfloat16>::value) {
+        w[i] = pack_bf16x2(f[2 * i], f[2 * i + 1]);
+      } else {
+        const __half2 v = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t*>(&v);
+      }
+    }
+  }
+};
+template <typename E>
+struct alignas(2) Pack<E, 1> {
+  uint16_t w;
+  __device__ __forceinline__ void get(float (&f)[1]) const {
+    if constexpr (std::is_same<E, __nv_bfloat16>::value)
+      f[0] = __uint_as_float(uint32_t(w) << 16);
+    else
+      f[0] = __half2float(__ushort_as_half(w));
+  }
+  __device__ __forceinline__ void set(const float (&f)[1]) {
+    if constexpr (std::is_same<E, __nv_bfloat16>::value)
+      w = __bfloat16_as_ushort(__float2bfloat16_rn(f[0]));
+    else
+      w = __half_as_ushort(__float2half_rn(f[0]));
+  }
+};
+// VEC 8-bit codes.
+template <int VEC>
+struct alignas(VEC) Codes {
+  uint8_t e[VEC];
+};
 
 // maximum that keeps a NaN
 __device__ __forceinline__ float max_nan(float a, float b) {
@@ -41,12 +88,6 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
   return r;
 }
-
-// VEC consecutive elements (16 bytes for VEC = 8, one element for VEC = 1)
-template <typename E, int VEC>
-struct alignas(sizeof(E) * VEC) Pack {
-  E e[VEC];
-};
 
 template <bool MAX>
 __device__ __forceinline__ float combine(float a, float b) {
@@ -102,6 +143,16 @@ __device__ __forceinline__ uint8_t code_of(float y, float inv) {
   }
 }
 
+template <typename E, int VEC>
+__device__ __forceinline__ void load_weight(const E* w, int p, float (&f)[VEC]) {
+  if (w != nullptr) {
+    reinterpret_cast<const Pack<E, VEC>*>(w)[p].get(f);
+  } else {
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) f[j] = 1.f;
+  }
+}
+
 // Whether a row's sum of squares left the range in which fp32 holds it well:
 // then the row is scaled by a power of two (row_scale) and summed again.
 __device__ __forceinline__ bool out_of_range(float ss) {
@@ -144,17 +195,18 @@ __global__ void __launch_bounds__(MAXT)
   for (int i = 0; i < NV; ++i) {
     const int p = i * blockDim.x + threadIdx.x;
     if (p < nvec) {
-      P& a = xa[i];
+      xa[i].get(v[i]);
       if (res != nullptr) {
+        float r[VEC];
+        ra[i].get(r);
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) a.e[j] = from_f32<E>(to_f32(a.e[j]) + to_f32(ra[i].e[j]));
-        *reinterpret_cast<P*>(s_out + base + static_cast<int64_t>(p) * VEC) = a;
+        for (int j = 0; j < VEC; ++j) v[i][j] += r[j];
+        xa[i].set(v[i]);
+        *reinterpret_cast<P*>(s_out + base + static_cast<int64_t>(p) * VEC) = xa[i];
+        xa[i].get(v[i]);
       }
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) {
-        v[i][j] = to_f32(a.e[j]);
-        ss += v[i][j] * v[i][j];
-      }
+      for (int j = 0; j < VEC; ++j) ss += v[i][j] * v[i][j];
     } else {
 #pragma unroll
       for (int j = 0; j < VEC; ++j) v[i][j] = 0.f;
@@ -191,11 +243,11 @@ __global__ void __launch_bounds__(MAXT)
   for (int i = 0; i < NV; ++i) {
     const int p = i * blockDim.x + threadIdx.x;
     if (p < nvec) {
-      P wv;
-      if (w != nullptr) wv = *reinterpret_cast<const P*>(w + static_cast<int64_t>(p) * VEC);
+      float wf[VEC];
+      load_weight<E, VEC>(w, p, wf);
 #pragma unroll
       for (int j = 0; j < VEC; ++j) {
-        v[i][j] = v[i][j] * rstd * (w != nullptr ? to_f32(wv.e[j]) : 1.f);
+        v[i][j] = v[i][j] * rstd * wf[j];
         amax = max_nan(amax, fabsf(v[i][j]));
       }
     }
@@ -206,8 +258,7 @@ __global__ void __launch_bounds__(MAXT)
       const int p = i * blockDim.x + threadIdx.x;
       if (p < nvec) {
         P o;
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) o.e[j] = from_f32<E>(v[i][j]);
+        o.set(v[i]);
         *reinterpret_cast<P*>(static_cast<E*>(out) + base + static_cast<int64_t>(p) * VEC) = o;
       }
     }
@@ -246,10 +297,10 @@ __global__ void __launch_bounds__(MAXT)
       }
       if (p < nvec) {
         const float inv = 1.f / scale;
-        Pack<uint8_t, VEC> o;
+        Codes<VEC> o;
 #pragma unroll
         for (int j = 0; j < VEC; ++j) o.e[j] = code_of<FMT>(v[i][j], inv);
-        *reinterpret_cast<Pack<uint8_t, VEC>*>(static_cast<uint8_t*>(out) + base +
+        *reinterpret_cast<Codes<VEC>*>(static_cast<uint8_t*>(out) + base +
                                                static_cast<int64_t>(p) * VEC) = o;
       }
     }
@@ -315,13 +366,14 @@ __global__ void __launch_bounds__(MAXT, backward_blocks(VEC, NV, MAXT))
     for (int i = 0; i < NV; ++i) {
       const int p = i * blockDim.x + threadIdx.x;
       if (p < nvec) {
-        P wv;
-        if (w != nullptr) wv = *reinterpret_cast<const P*>(w + static_cast<int64_t>(p) * VEC);
+        float a[VEC], d[VEC], wf[VEC];
+        sv[i].get(a);
+        dv[i].get(d);
+        load_weight<E, VEC>(w, p, wf);
 #pragma unroll
         for (int j = 0; j < VEC; ++j) {
-          const float a = to_f32(sv[i].e[j]);
-          ss += a * a;
-          sd += a * to_f32(dv[i].e[j]) * (w != nullptr ? to_f32(wv.e[j]) : 1.f);
+          ss += a[j] * a[j];
+          sd += a[j] * (d[j] * wf[j]);
         }
       }
     }
@@ -333,21 +385,27 @@ __global__ void __launch_bounds__(MAXT, backward_blocks(VEC, NV, MAXT))
       float amax = 0.f;
 #pragma unroll
       for (int i = 0; i < NV; ++i)
-        if (i * static_cast<int>(blockDim.x) + static_cast<int>(threadIdx.x) < nvec)
+        if (i * static_cast<int>(blockDim.x) + static_cast<int>(threadIdx.x) < nvec) {
+          float a[VEC];
+          sv[i].get(a);
 #pragma unroll
-          for (int j = 0; j < VEC; ++j) amax = max_nan(amax, fabsf(to_f32(sv[i].e[j])));
+          for (int j = 0; j < VEC; ++j) amax = max_nan(amax, fabsf(a[j]));
+        }
       mult = row_scale(block_reduce<true>(amax, red[2][0]), eps);
       ss = sd = 0.f;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const int p = i * blockDim.x + threadIdx.x;
         if (p < nvec) {
+          float a[VEC], d[VEC], wf[VEC];
+          sv[i].get(a);
+          dv[i].get(d);
+          load_weight<E, VEC>(w, p, wf);
 #pragma unroll
           for (int j = 0; j < VEC; ++j) {
-            const float a = to_f32(sv[i].e[j]) * mult;
-            ss += a * a;
-            sd += a * to_f32(dv[i].e[j]) *
-                  (w != nullptr ? to_f32(w[static_cast<int64_t>(p) * VEC + j]) : 1.f);
+            a[j] *= mult;
+            ss += a[j] * a[j];
+            sd += a[j] * (d[j] * wf[j]);
           }
         }
       }
@@ -356,22 +414,31 @@ __global__ void __launch_bounds__(MAXT, backward_blocks(VEC, NV, MAXT))
     }
     const float rstd = rsqrtf(ss / static_cast<float>(H) + eps * mult * mult);  // of s * mult
     const float m = sd * rstd / static_cast<float>(H);                          // mean(dn n)
+    const float scale = rstd * mult;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int p = i * blockDim.x + threadIdx.x;
       if (p < nvec) {
-        P wv, o;
-        if (w != nullptr) wv = *reinterpret_cast<const P*>(w + static_cast<int64_t>(p) * VEC);
         if (!AHEAD && dstream != nullptr)
           tv[i] = *reinterpret_cast<const P*>(dstream + base + static_cast<int64_t>(p) * VEC);
+        float a[VEC], d[VEC], wf[VEC], t[VEC];
+        sv[i].get(a);
+        dv[i].get(d);
+        load_weight<E, VEC>(w, p, wf);
+        if (dstream != nullptr) {
+          tv[i].get(t);
+        } else {
+#pragma unroll
+          for (int j = 0; j < VEC; ++j) t[j] = 0.f;
+        }
 #pragma unroll
         for (int j = 0; j < VEC; ++j) {
-          const float n = to_f32(sv[i].e[j]) * mult * rstd, d = to_f32(dv[i].e[j]);
-          dw[i][j] += d * n;
-          float r = rstd * mult * (d * (w != nullptr ? to_f32(wv.e[j]) : 1.f) - n * m);
-          if (dstream != nullptr) r += to_f32(tv[i].e[j]);
-          o.e[j] = from_f32<E>(r);
+          const float n = a[j] * scale;
+          dw[i][j] += d[j] * n;
+          t[j] += scale * (d[j] * wf[j] - n * m);
         }
+        P o;
+        o.set(t);
         *reinterpret_cast<P*>(dx + base + static_cast<int64_t>(p) * VEC) = o;
       }
     }
