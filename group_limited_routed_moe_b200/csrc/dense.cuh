@@ -30,7 +30,7 @@ namespace moe {
 namespace dense {
 
 constexpr unsigned kSiteEmpty = 40, kSiteFull = 41, kSiteTmemFull = 42, kSiteTmemEmpty = 43,
-                   kSiteDrain = 44, kSiteSmallFull = 45, kSiteSmallEmpty = 46, kSiteSmallDone = 47;
+                   kSiteDrain = 44, kSiteSmallFull = 45, kSiteSmallEmpty = 46, kSiteSmallDone = 47, kSiteSmallParts = 48;
 
 enum Kind { kF16Kind = 0, kI8Kind = 1 };                 // operand width: 16 or 8 bits
 enum Epi { kGated = 0, kPlain = 1, kDGate = 2, kScaled = 3 };
@@ -105,6 +105,17 @@ __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
                    : "memory");
 }
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// A cluster barrier that orders execution alone (no wait for this thread's
+// stores to global memory to be seen).
+__device__ __forceinline__ void cluster_sync_relaxed() {
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+}
 __device__ __forceinline__ uint32_t map_to_rank(uint32_t addr, uint32_t rank) {
   uint32_t r;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
@@ -113,13 +124,35 @@ __device__ __forceinline__ uint32_t map_to_rank(uint32_t addr, uint32_t rank) {
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
-__device__ __forceinline__ uint4 ld_cluster_v4(uint32_t addr) {
-  uint4 v;
-  asm volatile("ld.shared::cluster.v4.b32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "r"(addr)
-               : "memory");
-  return v;
+// Stores 16 bytes into the shared memory of a CTA of the cluster and completes
+// them on a barrier there.
+__device__ __forceinline__ void st_async_v4(uint32_t addr, uint32_t bar, uint32_t a, uint32_t b, uint32_t c,
+                                            uint32_t d) {
+  asm volatile(
+      "st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%2, %3, %4, %5}, [%1];" ::"r"(addr),
+      "r"(bar), "r"(a), "r"(b), "r"(c), "r"(d)
+      : "memory");
+}
+// mbar_wait for a barrier that other CTAs of the cluster complete with data.
+__device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
+                                                  uint64_t timeout_ns, unsigned site) {
+  const uint64_t t0 = global_timer_ns();
+  for (uint32_t n = 1;; ++n) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    if (ok) return true;
+    if ((n & 31u) == 0 && global_timer_ns() - t0 > timeout_ns) {
+      record_status(site);
+      *abort_flag = 1;
+      return false;
+    }
+  }
 }
 // TMA load into this CTA's shared memory that signals `bar` (a shared::cluster
 // address: the barrier of either CTA of the pair).
@@ -616,7 +649,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
   }
   tc_fence_before();
   __syncwarp();
-  cluster_sync();  // neither CTA leaves while the other may still signal it
+  cluster_sync_relaxed();  // neither CTA leaves while the other may still signal it
   if (warp == kMmaWarp) {
     tc_fence_after();
     tmem_dealloc_pair(tmem, C::TMEM);

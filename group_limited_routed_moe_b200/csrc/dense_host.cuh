@@ -207,19 +207,19 @@ int launch_pair(const Product& p, int sms, cudaStream_t s) {
                     dim3(dense::kPairThreads), smem, s, g);
 }
 
-template <int KIND, bool W_MN, int EPI, int NT>
-int launch_small_nt(const Product& p, int sms, cudaStream_t s) {
+template <int KIND, bool W_MN, int EPI, int NT, int ROWS>
+int launch_small_rows(const Product& p, int sms, cudaStream_t s) {
   const int elem = KIND == dense::kI8Kind ? 1 : 2, ke = 128 / elem;
   dense::SmallArgs g{};
   g.T = p.a[0].outer();
   g.N = p.b[0].outer();
   g.nseg = p.nseg;
   g.kblocks = static_cast<int>(div_up(p.a[0].k(), ke));
-  g.wt = static_cast<int>(div_up(g.N, EPI == dense::kGated ? 64 : dense::kSmallRows));
+  g.wt = static_cast<int>(div_up(g.N, EPI == dense::kGated ? 64 : ROWS));
   const int64_t tiles = g.wt * div_up(g.T, NT);
   for (int i = 0; i < p.nseg; ++i) {
     int rc = make_map(&g.x[i], p.a[i].p, p.a[i].rows, p.a[i].cols, elem, NT);
-    if (!rc) rc = make_map(&g.w[i], p.b[i].p, p.b[i].rows, p.b[i].cols, elem, W_MN ? 64 : dense::kSmallRows);
+    if (!rc) rc = make_map(&g.w[i], p.b[i].p, p.b[i].rows, p.b[i].cols, elem, W_MN ? 64 : ROWS);
     if (rc) return rc;
   }
   if (EPI == dense::kGated) {
@@ -233,11 +233,11 @@ int launch_small_nt(const Product& p, int sms, cudaStream_t s) {
   g.early = p.early;
   g.out = p.out[0];
   common_args(&g, p);
-  g.idesc = dense::make_idesc(KIND, p.type, W_MN, false, dense::kSmallRows, NT);
+  g.idesc = dense::make_idesc(KIND, p.type, W_MN, false, 128, NT);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(tiles * g.split));
   cfg.blockDim = dim3(dense::kSmallThreads);
-  cfg.dynamicSmemBytes = dense::SmallCfg<NT>::SMEM;
+  cfg.dynamicSmemBytes = dense::SmallCfg<NT, ROWS>::SMEM;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -248,9 +248,20 @@ int launch_small_nt(const Product& p, int sms, cudaStream_t s) {
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, dense::small_gemm_kernel<KIND, W_MN, EPI, NT>, g);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, dense::small_gemm_kernel<KIND, W_MN, EPI, NT, ROWS>, g);
   if (e != cudaSuccess) return cuda_fail(e, "small_gemm_kernel launch");
   return MOE_OK;
+}
+
+template <int KIND, bool W_MN, int EPI, int NT>
+int launch_small_nt(const Product& p, int sms, cudaStream_t s) {
+  if constexpr (EPI != dense::kGated) {
+    // tiles of 64 weight rows where 128-row tiles, split as far as they go,
+    // are fewer than the SMs
+    const int64_t tiles = div_up(p.b[0].outer(), 128) * div_up(p.a[0].outer(), NT);
+    if (tiles * dense::kMaxSplit < sms) return launch_small_rows<KIND, W_MN, EPI, NT, 64>(p, sms, s);
+  }
+  return launch_small_rows<KIND, W_MN, EPI, NT, 128>(p, sms, s);
 }
 
 template <int KIND, bool B_MN, int EPI>
@@ -274,8 +285,13 @@ cudaError_t pair_attr() {
 }
 template <int KIND, bool W_MN, int EPI, int NT>
 cudaError_t small_attr_nt() {
-  return cudaFuncSetAttribute(dense::small_gemm_kernel<KIND, W_MN, EPI, NT>,
-                              cudaFuncAttributeMaxDynamicSharedMemorySize, dense::SmallCfg<NT>::SMEM);
+  cudaError_t e = cudaFuncSetAttribute(dense::small_gemm_kernel<KIND, W_MN, EPI, NT, 128>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, dense::SmallCfg<NT, 128>::SMEM);
+  if constexpr (EPI != dense::kGated)
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(dense::small_gemm_kernel<KIND, W_MN, EPI, NT, 64>,
+                               cudaFuncAttributeMaxDynamicSharedMemorySize, dense::SmallCfg<NT, 64>::SMEM);
+  return e;
 }
 template <int KIND, bool W_MN, int EPI>
 cudaError_t small_attr() {

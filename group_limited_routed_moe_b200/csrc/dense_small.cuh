@@ -4,11 +4,13 @@
 // The weights are the 128-row operand of the MMA (their n on the accumulator's
 // lanes) and up to NT tokens its columns, so no tensor-core row is spent on
 // padding tokens, and 128 x K weight bytes stream through each CTA.  With few
-// weight tiles the k range is split over the CTAs of a cluster: each leaves its
-// partial accumulators in its shared memory, and after a cluster barrier every
-// CTA adds up its share of the outputs from all of them, in rank order (so the
-// result does not depend on timing), and runs the epilogue on it.  One launch,
-// no workspace, no atomics.
+// weight tiles the k range is split over the CTAs of a cluster.  Each CTA owns
+// a share of the tile's outputs; every CTA sends the parts of its accumulators
+// to their owners' shared memory (st.async, counted on the owner's barrier),
+// and the owner adds them up in rank order, so the result does not depend on
+// timing, and runs the epilogue.  One launch, no workspace, no atomics, and no
+// cluster barrier after the products: gathering by a barrier, loads from the
+// other CTAs and a second barrier took 1.5 us more of a 6 us launch.
 #pragma once
 #include "dense.cuh"
 
@@ -17,21 +19,27 @@ namespace dense {
 
 constexpr int kSmallThreads = 256;
 constexpr int kMaxSplit = 8;
-constexpr int kSmallRows = 128;  // weight rows of a tile (kGated: 64 gate and 64 up columns)
 
-template <int NT>
+// ROWS weight rows of a tile: 128 (kGated: 64 gate and 64 up columns), or 64
+// where tiles of 128 cannot occupy the SMs.  The MMA is 128 rows high in both
+// cases; with 64 the upper accumulator rows are products of whatever lies
+// behind the weights in shared memory, and are not read.
+template <int NT, int ROWS>
 struct SmallCfg {
-  static constexpr int STAGE = kSmallRows * kKB + NT * kKB;
-  // up to 110 KB a CTA, so that two share an SM (and the next launch's CTAs
-  // can start reading while the last ones of this one finish)
-  static constexpr int STAGES = NT <= 32 ? 5 : NT == 64 ? 4 : 3;
-  static constexpr int PART = NT * kSmallRows * 4;  // reuses the stages' memory
-  static constexpr int SMEM = STAGES * STAGE + 1024 + 256;
+  static constexpr int STAGE = ROWS * kKB + NT * kKB;
+  // few stages: up to 32 tokens three CTAs fit on an SM, so that the next
+  // launch's CTAs can already read weights while this one's finish
+  static constexpr int STAGES = ROWS == 64 && NT <= 32 ? 5 : 3;
+  // tokens of a part's row, 4 more than there are: 8 rows of 16 bytes then lie
+  // in different banks
+  static constexpr int PITCH = NT + 4;
+  static constexpr int PART = ROWS * PITCH * 4;
+  static constexpr int SMEM = STAGES * STAGE + PART + 1024 + 256 + (ROWS == 64 ? 1024 : 0);
   static constexpr int TMEM = NT < 32 ? 32 : NT;
-  static_assert(PART <= STAGES * STAGE, "partial sums fit the stages");
+  static_assert((STAGES - 1) * STAGE + 128 * kKB <= SMEM - 1024, "the MMA's rows stay inside");
 };
 struct SmallTail {
-  uint64_t full[8], empty[8], done;
+  uint64_t full[8], empty[8], done, parts;
   uint32_t tmem_base;
   int abort_flag;
 };
@@ -54,19 +62,24 @@ struct SmallArgs {
   uint64_t timeout_ns;
 };
 
-template <int KIND, bool W_MN, int EPI, int NT>
+template <int KIND, bool W_MN, int EPI, int NT, int ROWS>
 __global__ void __launch_bounds__(kSmallThreads)
     small_gemm_kernel(const __grid_constant__ SmallArgs g) {
-  using C = SmallCfg<NT>;
+  using C = SmallCfg<NT, ROWS>;
+  static_assert(EPI != kGated || ROWS == 128, "64 gate and 64 up columns");
   constexpr int KE = KIND == kI8Kind ? 128 : 64;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  SmallTail* S = reinterpret_cast<SmallTail*>(smem + C::STAGES * C::STAGE);
+  uint8_t* sPart = smem + C::STAGES * C::STAGE;
+  SmallTail* S = reinterpret_cast<SmallTail*>(sPart + C::PART);
   volatile int* abort_flag = &S->abort_flag;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = blockIdx.x % g.split, tile = blockIdx.x / g.split;
   const int wtile = tile % g.wt, ttile = tile / g.wt;
+  const int64_t t0 = int64_t(ttile) * NT;
+  const int ntok = static_cast<int>(min(int64_t(NT), g.T - t0));
+  const int ngrp = (ntok + 3) / 4;  // tokens are sent four at a time
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::STAGES; ++s) {
@@ -74,8 +87,10 @@ __global__ void __launch_bounds__(kSmallThreads)
       mbar_init(&S->empty[s], 1);
     }
     mbar_init(&S->done, 1);
+    mbar_init(&S->parts, 1);
     S->abort_flag = 0;
     fence_barrier_init();
+    mbar_arrive_expect_tx(&S->parts, ngrp * ROWS * 16);
   }
   if (warp == 0 && lane == 0) {
     for (int i = 0; i < g.nseg; ++i) tma_prefetch_desc(&g.x[i]);
@@ -88,6 +103,7 @@ __global__ void __launch_bounds__(kSmallThreads)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = S->tmem_base;
+  cluster_arrive();  // waited for before anything is sent: the barriers of all ranks exist then
 
   // this CTA's k-blocks: an even share of all segments' blocks
   const int kbs = g.kblocks * g.nseg;
@@ -103,10 +119,11 @@ __global__ void __launch_bounds__(kSmallThreads)
       tma_load_2d(sw, &g.w[0], wtile * 64, k0, &S->full[s]);
       tma_load_2d(sw + 8192, &g.w[1], wtile * 64, k0, &S->full[s]);
     } else if constexpr (W_MN) {
-      tma_load_2d(sw, &g.w[seg], wtile * 128, k0, &S->full[s]);
-      tma_load_2d(sw + 8192, &g.w[seg], wtile * 128 + 64, k0, &S->full[s]);
+#pragma unroll
+      for (int c = 0; c < ROWS / 64; ++c)
+        tma_load_2d(sw + c * 8192, &g.w[seg], wtile * ROWS + c * 64, k0, &S->full[s]);
     } else {
-      tma_load_2d(sw, &g.w[seg], k0, wtile * 128, &S->full[s]);
+      tma_load_2d(sw, &g.w[seg], k0, wtile * ROWS, &S->full[s]);
     }
   };
   // Where the launch before this one is a step of the same call (which waited
@@ -117,6 +134,38 @@ __global__ void __launch_bounds__(kSmallThreads)
     for (; ahead < C::STAGES && kb0 + ahead < kb1; ++ahead) load_w(kb0 + ahead, ahead);
   griddep_wait();
   griddep_launch_dependents();
+
+  // The outputs this CTA owns: unit e is column e % own of its share and the 4
+  // tokens from e / own * 4 on.  What the epilogue reads of a thread's next
+  // unit is loaded ahead, the first one's before the products.
+  constexpr int PER = EPI == kGated ? 64 : ROWS;
+  const int own = PER / g.split;                // output columns a rank owns
+  const int rows = ROWS / g.split;              // rows of a part
+  const uint32_t parts = smem_u32(sPart);
+  const int64_t col0 = int64_t(wtile) * PER + rank * own;
+  float pre[EPI == kScaled ? 6 : EPI == kDGate ? 8 : EPI == kPlain ? 4 : 1];
+  auto fetch = [&](int e) {
+    const int64_t col = col0 + e % own;
+    const int tok = e / own * 4;
+    if (e >= ngrp * own || col >= g.N) return;
+    if constexpr (EPI == kScaled) {
+      pre[4] = g.b_scale[col];
+      pre[5] = g.bias != nullptr ? g.bias[col] : 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int64_t row = t0 + min(tok + i, ntok - 1);
+      if constexpr (EPI == kScaled) pre[i] = g.a_scale[row];
+      if constexpr (EPI == kPlain)
+        pre[i] = g.residual != nullptr ? unpack1(g.residual[row * g.N + col], g.type) : 0.f;
+      if constexpr (EPI == kDGate) {
+        const uint8_t* sv = g.saved + saved_block(row, col, g.N) + saved_word(row, col);
+        saved_get(*reinterpret_cast<const uint16_t*>(sv), *reinterpret_cast<const uint16_t*>(sv + kSavedPlane),
+                  *reinterpret_cast<const uint16_t*>(sv + 2 * kSavedPlane), 0, pre[i], pre[4 + i]);
+      }
+    }
+  };
+  fetch(threadIdx.x);
 
   if (warp == 0) {
     if (lane == 0) {
@@ -131,7 +180,7 @@ __global__ void __launch_bounds__(kSmallThreads)
         const int seg = kb >= g.kblocks ? 1 : 0;
         const int k0 = (kb - seg * g.kblocks) * KE;
         if (it >= ahead) load_w(kb, s);
-        tma_load_2d(smem_u32(smem + s * C::STAGE) + kSmallRows * kKB, &g.x[seg], k0, ttile * NT, &S->full[s]);
+        tma_load_2d(smem_u32(smem + s * C::STAGE) + ROWS * kKB, &g.x[seg], k0, ttile * NT, &S->full[s]);
       }
       if (!ok)  // let the copies already issued land before the block can exit
         for (int i = max(0, it - C::STAGES); i < it; ++i)
@@ -145,7 +194,7 @@ __global__ void __launch_bounds__(kSmallThreads)
         if (!mbar_wait(&S->full[s], (it / C::STAGES) & 1, abort_flag, g.timeout_ns, kSiteSmallFull)) break;
         tc_fence_after();
         const uint32_t sw = smem_u32(smem + s * C::STAGE);
-        const uint64_t dw = operand_desc<W_MN>(sw), dx = operand_desc<false>(sw + kSmallRows * kKB);
+        const uint64_t dw = operand_desc<W_MN>(sw), dx = operand_desc<false>(sw + ROWS * kKB);
 #pragma unroll
         for (int k = 0; k < 4; ++k)
           umma_single<KIND>(tmem, dw + k * kDescStep<W_MN>, dx + k * kDescStep<false>, g.idesc, (it | k) != 0);
@@ -159,12 +208,17 @@ __global__ void __launch_bounds__(kSmallThreads)
   ok = __syncthreads_and(ok && !*abort_flag) != 0;
   tc_fence_after();
 
-  // accumulators -> this CTA's partial sums [token][weight row], fp32 (or int32)
-  uint32_t* part = reinterpret_cast<uint32_t*>(smem);
-  if (ok && kb1 > kb0) {
-    const int quarter = warp & 3;
-#pragma unroll
-    for (int c = (warp >> 2) * 8; c < NT; c += 16) {
+  // accumulators -> their owners: weight row r (kGated: gate row r and up row
+  // 64 + r) belongs to rank r / OWN.  A CTA without k-blocks, or whose wait ran
+  // out, sends zeros, so that no owner waits for it in vain.
+  cluster_wait();
+  {
+    const int quarter = warp & 3, r = quarter * 32 + lane;
+    const int owner = r % PER / own, local = r / PER * own + r % PER % own;
+    const uint32_t to = map_to_rank(parts + (rank * rows + local) * C::PITCH * 4, owner);
+    const uint32_t bar = map_to_rank(smem_u32(&S->parts), owner);
+    const bool have = ok && kb1 > kb0;
+    for (int c = (warp >> 2) * 8; c < ntok && quarter * 32 < ROWS; c += 16) {
       uint32_t v[8];
       asm volatile(
           "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n\t"
@@ -173,113 +227,80 @@ __global__ void __launch_bounds__(kSmallThreads)
           : "r"(tmem + c + (uint32_t(quarter * 32) << 16))
           : "memory");
 #pragma unroll
-      for (int i = 0; i < 8; ++i) part[(c + i) * kSmallRows + quarter * 32 + lane] = v[i];
+      for (int h = 0; h < 2; ++h)
+        if (c + 4 * h < ntok)
+          st_async_v4(to + (c + 4 * h) * 4, bar, have ? v[4 * h] : 0u, have ? v[4 * h + 1] : 0u,
+                      have ? v[4 * h + 2] : 0u, have ? v[4 * h + 3] : 0u);
     }
-  } else {  // no k-blocks (or a wait that ran out): zeros
-    for (int i = threadIdx.x; i < NT * kSmallRows; i += kSmallThreads) part[i] = 0u;
   }
   tc_fence_before();
-  if (g.split > 1) cluster_sync(); else __syncthreads();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::TMEM);
+  }
+  // every rank sends within its own waits' limits
+  if (!mbar_wait_cluster(&S->parts, 0, abort_flag, 4 * g.timeout_ns, kSiteSmallParts)) return;
 
-  // A share of the outputs: unit e is 4 consecutive weight rows of a token.  All
-  // ranks' parts of a unit are loaded before they are added up (one after the
-  // other, each load from another SM's memory would cost its full latency).
-  constexpr int PER = EPI == kGated ? 64 : kSmallRows, UNITS = PER / 4;
-  const int64_t t0 = int64_t(ttile) * NT;
-  const int ntok = static_cast<int>(min(int64_t(NT), g.T - t0));
-  const uint32_t mine = smem_u32(part);
-  auto total = [&](int index, float (&sum)[4]) {  // sums over the ranks, in rank order
-    uint4 v[kMaxSplit];
-#pragma unroll
-    for (int r = 0; r < kMaxSplit; ++r)
-      if (r < g.split) v[r] = ld_cluster_v4(map_to_rank(mine + index * 4, r));
+  auto total = [&](int local, int grp, float (&sum)[4]) {  // sums over the ranks, in rank order
+    const uint32_t at = parts + (local * C::PITCH + grp * 4) * 4;
     if constexpr (KIND == kI8Kind) {
       int a[4] = {0, 0, 0, 0};
-#pragma unroll
-      for (int r = 0; r < kMaxSplit; ++r)
-        if (r < g.split) {
-          a[0] += int(v[r].x); a[1] += int(v[r].y); a[2] += int(v[r].z); a[3] += int(v[r].w);
-        }
+#pragma unroll 4
+      for (int r = 0; r < g.split; ++r) {
+        const uint4 v = ld_shared_v4(at + r * rows * C::PITCH * 4);
+        a[0] += int(v.x); a[1] += int(v.y); a[2] += int(v.z); a[3] += int(v.w);
+      }
 #pragma unroll
       for (int i = 0; i < 4; ++i) sum[i] = static_cast<float>(a[i]);
     } else {
 #pragma unroll
       for (int i = 0; i < 4; ++i) sum[i] = 0.f;
-#pragma unroll
-      for (int r = 0; r < kMaxSplit; ++r)
-        if (r < g.split) {
-          sum[0] += __uint_as_float(v[r].x); sum[1] += __uint_as_float(v[r].y);
-          sum[2] += __uint_as_float(v[r].z); sum[3] += __uint_as_float(v[r].w);
-        }
+#pragma unroll 4
+      for (int r = 0; r < g.split; ++r) {
+        const uint4 v = ld_shared_v4(at + r * rows * C::PITCH * 4);
+        sum[0] += __uint_as_float(v.x); sum[1] += __uint_as_float(v.y);
+        sum[2] += __uint_as_float(v.z); sum[3] += __uint_as_float(v.w);
+      }
     }
   };
-  for (int e = rank * kSmallThreads + threadIdx.x; e < ntok * UNITS; e += g.split * kSmallThreads) {
-    const int tok = e / UNITS, r = e % UNITS * 4;
-    const int64_t col = int64_t(wtile) * PER + r, row = t0 + tok;
-    if (col >= g.N) continue;
-    const int64_t at = row * g.N + col;
-    float y[4], z[4];
-    total(tok * kSmallRows + r, y);
-    if constexpr (EPI == kScaled) {
-      const float sa = g.a_scale[row];
-      // rows of any length: element by element
+  for (int e = threadIdx.x; e < ngrp * own; e += kSmallThreads) {
+    const int local = e % own, grp = e / own;
+    const int64_t col = col0 + local;
+    if (col < g.N) {
+      float y[4], z[4];
+      total(local, grp, y);
+      if constexpr (EPI == kGated) total(own + local, grp, z);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        if (col + i >= g.N) break;
-        const float v = fmaf(y[i] * sa, g.b_scale[col + i], g.bias != nullptr ? g.bias[col + i] : 0.f);
-        if (g.type == kF32)
-          static_cast<float*>(g.out)[at + i] = v;
-        else
-          static_cast<uint16_t*>(g.out)[at + i] = pack1(v, g.type);
-      }
-    } else {  // N is a multiple of 8
-      uint8_t* sv = nullptr;
-      if constexpr (EPI != kPlain)
-        if (g.saved != nullptr) sv = g.saved + saved_block(row, col, g.N) + saved_word(row, col);
-      if constexpr (EPI == kGated) {
-        total(tok * kSmallRows + 64 + r, z);
-        if (sv != nullptr) {
-          uint32_t w[4], l[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            w[i] = __float_as_uint(y[i]);
-            l[i] = __float_as_uint(z[i]);
+        const int64_t row = t0 + grp * 4 + i, at = row * g.N + col;
+        if (grp * 4 + i >= ntok) break;
+        if constexpr (EPI == kGated) {
+          if (g.saved != nullptr) {
+            uint8_t* sv = g.saved + saved_block(row, col, g.N) + saved_word(row, col);
+            const uint32_t gb = __float_as_uint(y[i]), ub = __float_as_uint(z[i]);
+            *reinterpret_cast<uint16_t*>(sv) = static_cast<uint16_t>(gb >> 16);
+            *reinterpret_cast<uint16_t*>(sv + kSavedPlane) = static_cast<uint16_t>(ub >> 16);
+            *reinterpret_cast<uint16_t*>(sv + 2 * kSavedPlane) = static_cast<uint16_t>(saved_low(gb, ub, 0u, 0u));
           }
-          *reinterpret_cast<uint2*>(sv) = make_uint2((w[0] >> 16) | (w[1] & 0xFFFF0000u), (w[2] >> 16) | (w[3] & 0xFFFF0000u));
-          *reinterpret_cast<uint2*>(sv + kSavedPlane) =
-              make_uint2((l[0] >> 16) | (l[1] & 0xFFFF0000u), (l[2] >> 16) | (l[3] & 0xFFFF0000u));
-          *reinterpret_cast<uint2*>(sv + 2 * kSavedPlane) = make_uint2(saved_low(w[0], l[0], w[1], l[1]), saved_low(w[2], l[2], w[3], l[3]));
+          y[i] = silu(y[i]) * z[i];
+        } else if constexpr (EPI == kPlain) {
+          y[i] += pre[i];
+        } else if constexpr (EPI == kDGate) {
+          float du;
+          dgate(y[i], pre[i], pre[4 + i], y[i], du);
+          static_cast<uint16_t*>(g.out2)[at] = pack1(du, g.type);
+        } else {
+          y[i] = fmaf(y[i] * pre[i], pre[4], pre[5]);
+          if (g.type == kF32) {
+            static_cast<float*>(g.out)[at] = y[i];
+            continue;
+          }
         }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) y[i] = silu(y[i]) * z[i];
-      } else if constexpr (EPI == kPlain) {
-        if (g.residual != nullptr) {
-          const uint2 q = *reinterpret_cast<const uint2*>(g.residual + at);
-          y[0] += unpack_lo(q.x, g.type); y[1] += unpack_hi(q.x, g.type);
-          y[2] += unpack_lo(q.y, g.type); y[3] += unpack_hi(q.y, g.type);
-        }
-      } else {
-        const uint2 gh = *reinterpret_cast<const uint2*>(sv), uh = *reinterpret_cast<const uint2*>(sv + kSavedPlane),
-                    lo = *reinterpret_cast<const uint2*>(sv + 2 * kSavedPlane);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          float gg, uu;
-          saved_get((&gh.x)[i / 2], (&uh.x)[i / 2], (&lo.x)[i / 2], i % 2, gg, uu);
-          dgate(y[i], gg, uu, y[i], z[i]);
-        }
-        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(g.out2) + at) =
-            make_uint2(pack2(z[0], z[1], g.type), pack2(z[2], z[3], g.type));
+        static_cast<uint16_t*>(g.out)[at] = pack1(y[i], g.type);
       }
-      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(g.out) + at) =
-          make_uint2(pack2(y[0], y[1], g.type), pack2(y[2], y[3], g.type));
     }
-  }
-  // a peer may still read this CTA's partial sums
-  __syncwarp();
-  if (g.split > 1) cluster_sync(); else __syncthreads();
-  if (warp == 1) {
-    tc_fence_after();
-    tmem_dealloc(tmem, C::TMEM);
+    fetch(e + kSmallThreads);
   }
 }
 
