@@ -22,7 +22,10 @@
 // holds the accumulators of its 128 rows, so a byte of B in shared memory
 // feeds twice the MMAs of a single-CTA tile.  Persistent, tiles round-robin;
 // two accumulator sets, so the epilogue of one tile overlaps the next one's
-// MMAs.
+// MMAs.  Where the tiles are too few for the SMs, 2 to 4 pairs of a larger
+// cluster share a tile (`split`): each takes a range of k and sends its
+// accumulators, by 32 columns, to the pair that owns these columns, which adds
+// them up in rank order and stores them.
 #pragma once
 #include "common.cuh"
 
@@ -30,7 +33,7 @@ namespace moe {
 namespace dense {
 
 constexpr unsigned kSiteEmpty = 40, kSiteFull = 41, kSiteTmemFull = 42, kSiteTmemEmpty = 43,
-                   kSiteDrain = 44, kSiteSmallFull = 45, kSiteSmallEmpty = 46, kSiteSmallDone = 47, kSiteSmallParts = 48;
+                   kSiteDrain = 44, kSiteSmallFull = 45, kSiteSmallEmpty = 46, kSiteSmallDone = 47, kSiteSmallParts = 48, kSiteParts = 49;
 
 enum Kind { kF16Kind = 0, kI8Kind = 1 };                 // operand width: 16 or 8 bits
 enum Epi { kGated = 0, kPlain = 1, kDGate = 2, kScaled = 3 };
@@ -58,15 +61,17 @@ __device__ __forceinline__ int saved_word(int64_t row, int64_t col) {
   return static_cast<int>(((col & 31) >> 3) * 512 + (row & 31) * 16 + (col & 7) * 2);
 }
 
-// The low-plane words of two neighbouring columns (e, o) from the fp32 bits of g and u.
+// The planes' words of two neighbouring columns (e, o) from the fp32 bits of g
+// and u.
+__device__ __forceinline__ uint32_t saved_high(uint32_t e, uint32_t o) { return __byte_perm(e, o, 0x7632); }
 __device__ __forceinline__ uint32_t saved_low(uint32_t ge, uint32_t ue, uint32_t go, uint32_t uo) {
-  return ((ge >> 8) & 0xFFu) | (ue & 0xFF00u) | ((go << 8) & 0xFF0000u) | ((uo << 16) & 0xFF000000u);
+  return __byte_perm(__byte_perm(ge, ue, 0x0051), __byte_perm(go, uo, 0x0051), 0x5410);
 }
-// g and u of column j (0, 1) of a pair of words.
+// g and u of column j (0, 1) of a pair of words.  The low byte that was cut
+// repeats the one above it: a byte of zeros would take a second instruction.
 __device__ __forceinline__ void saved_get(uint32_t gh, uint32_t uh, uint32_t lo, int j, float& g, float& u) {
-  const uint32_t l = lo >> (16 * j);
-  g = __uint_as_float((j ? gh & 0xFFFF0000u : gh << 16) | ((l & 0xFFu) << 8));
-  u = __uint_as_float((j ? uh & 0xFFFF0000u : uh << 16) | (l & 0xFF00u));
+  g = __uint_as_float(__byte_perm(gh, lo, j ? 0x3266 : 0x1044));
+  u = __uint_as_float(__byte_perm(uh, lo, j ? 0x3277 : 0x1055));
 }
 
 struct Problem {
@@ -84,6 +89,7 @@ struct Args {
   int nseg;        // k segments of one product (a[i], b[i] summed), 1 or 2; nprob 1 then
   int kblocks;     // k-blocks of a segment
   int tiles;
+  int split;       // pairs that share a tile, 1 .. 4; with more than one, a cluster per tile
   int type;        // 16-bit type of operands and outputs (Type), or kF32 outputs (kScaled)
   uint32_t idesc;
   const uint16_t* residual;        // kPlain: [M][N] or NULL
@@ -192,12 +198,13 @@ __device__ __forceinline__ void umma_single(uint32_t d, uint64_t a, uint64_t b, 
         "l"(a), "l"(b), "r"(idesc), "r"(acc)
         : "memory");
 }
-// Arrives on the barrier at this offset in both CTAs of the pair.
-__device__ __forceinline__ void umma_commit_pair(uint64_t* bar) {
+// Arrives on the barrier at this offset in both CTAs of the pair, ranks lead
+// and lead + 1 of the cluster.
+__device__ __forceinline__ void umma_commit_pair(uint64_t* bar, uint32_t lead) {
   asm volatile(
       "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
       " [%0], %1;" ::"r"(smem_u32(bar)),
-      "h"(static_cast<uint16_t>(3))
+      "h"(static_cast<uint16_t>(3u << lead))
       : "memory");
 }
 __device__ __forceinline__ void tmem_alloc_pair(uint32_t* slot, uint32_t ncols) {
@@ -256,16 +263,25 @@ __device__ __forceinline__ float unpack1(uint16_t v, int type) {
   return type == kF16 ? __half2float(__ushort_as_half(v)) : __uint_as_float(uint32_t(v) << 16);
 }
 
-// For very negative g the exponential overflows to infinity and the quotient
-// is 0, the limit.
-__device__ __forceinline__ float sigmoid(float g) { return __fdividef(1.0f, 1.0f + __expf(-g)); }
-__device__ __forceinline__ float silu(float g) { return __fdividef(g, 1.0f + __expf(-g)); }
+// 1 / (1 + e^-g) by the approximate exponential and reciprocal (2^-21 together;
+// the 16-bit rounding that follows is 2^-11 at best), results below 2^-126
+// flushed: without the flush their range handling was half of the epilogues'
+// instructions.  For very negative g the exponential is infinite and the
+// quotient 0, the limit.
+__device__ __forceinline__ float sigmoid(float g) {
+  float e, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950408889634f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+  return r;
+}
+__device__ __forceinline__ float silu(float g) { return g * sigmoid(g); }
 
-// Gradients of silu(g) * u: du = dh silu(g), dg = dh u silu'(g).
+// Gradients of silu(g) * u: du = dh silu(g), dg = dh u silu'(g), where
+// silu' = s + g s (1 - s) = s (1 + g (1 - s)).
 __device__ __forceinline__ void dgate(float dh, float g, float u, float& dg, float& du) {
-  const float s = sigmoid(g), act = g * s;
-  du = dh * act;
-  dg = dh * u * (s + act * (1.f - s));
+  const float s = sigmoid(g);
+  du = dh * (g * s);
+  dg = (dh * u) * (s * fmaf(g, 1.f - s, 1.f));
 }
 
 // 32 consecutive fp32 columns of the calling warp's 32 TMEM lanes.
@@ -349,6 +365,8 @@ constexpr int kBM = 256;          // tile rows (128 per CTA)
 constexpr int kEpiWarps = 8;      // two per 32-lane quarter of tensor memory, a half of the columns each
 constexpr int kPairThreads = 32 * (kEpiWarps + 2);
 constexpr int kABytes = 128 * kKB;
+constexpr int kPartBytes = 8 * 128 * 16;  // 32 accumulator columns of 128 rows
+constexpr int kMaxPairs = 4;               // pairs of a cluster (of 8 CTAs)
 template <int BN>
 struct PairCfg {
   static constexpr int B_BYTES = BN / 2 * kKB;
@@ -359,7 +377,7 @@ struct PairCfg {
   static constexpr int SMEM = STAGES * STAGE + kEpiWarps * kStageWarp + 1024 + 256;
 };
 struct PairTail {
-  uint64_t full[8], empty[8], tfull[2], tempty[2], drain;
+  uint64_t full[8], empty[8], tfull[2], tempty[2], drain, parts;
   uint32_t tmem_base;
   int abort_flag;
 };
@@ -380,7 +398,7 @@ __device__ __forceinline__ void decode(const Args& g, int t, int& q, int& m, int
 }
 
 template <int KIND, bool A_MN, bool B_MN, int EPI, int BN>
-__global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
+__global__ void __launch_bounds__(kPairThreads, 1)
     pair_gemm_kernel(const __grid_constant__ Args g) {
   using C = PairCfg<BN>;
   constexpr int KE = KIND == kI8Kind ? 128 : 64;  // elements of a k-block
@@ -391,7 +409,11 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
   PairTail* S = reinterpret_cast<PairTail*>(sEpi + kEpiWarps * kStageWarp);
   volatile int* abort_flag = &S->abort_flag;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t rank = cluster_rank();
+  // rank in the pair, the pair in the cluster, the cluster rank of its CTA 0
+  const uint32_t crank = cluster_rank(), rank = crank & 1, pair = crank >> 1, lead = crank & ~1u;
+  // 32-column chunks of a tile's output, and those this pair stores
+  constexpr int NCH = (EPI == kGated ? BN / 2 : BN) / 32, G = EPI == kGated ? 2 : 1;
+  const int chunk0 = NCH * pair / g.split, chunk1 = NCH * (pair + 1) / g.split;
   constexpr int kTmaWarp = kEpiWarps, kMmaWarp = kEpiWarps + 1;
 
   if (threadIdx.x == 0) {
@@ -404,8 +426,10 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
       mbar_init(&S->tempty[a], 2 * kEpiWarps);
     }
     mbar_init(&S->drain, 1);
+    mbar_init(&S->parts, 1);
     S->abort_flag = 0;
     fence_barrier_init();
+    mbar_arrive_expect_tx(&S->parts, (g.split - 1) * (chunk1 - chunk0) * G * kPartBytes);
   }
   if (warp == kTmaWarp && lane == 0) {
     for (int i = 0; i < kMaxProb; ++i) {
@@ -416,14 +440,14 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
   __syncwarp();
   if (warp == kMmaWarp) tmem_alloc_pair(&S->tmem_base, C::TMEM);
   tc_fence_before();
-  cluster_sync();  // barriers of both CTAs exist before either signals the other
+  cluster_sync();  // every CTA's barriers exist before another signals them
   tc_fence_after();
   const uint32_t tmem = S->tmem_base;
   griddep_wait();
   griddep_launch_dependents();
 
-  const int cluster = blockIdx.x >> 1, nclusters = gridDim.x >> 1;
-  const int kbs = g.kblocks * g.nseg;
+  const int cluster = blockIdx.x / (2 * g.split), nclusters = gridDim.x / (2 * g.split);
+  const int kbs = g.kblocks * g.nseg, kb0 = kbs * pair / g.split, kb1 = kbs * (pair + 1) / g.split;
 
   if (warp == kTmaWarp) {
     if (lane == 0) {
@@ -435,7 +459,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
         const int m0 = m * kBM + static_cast<int>(rank) * 128;
         // kGated: CTA 0 brings the gate columns, CTA 1 the up columns
         const int n0 = EPI == kGated ? n * (BN / 2) : n * BN + static_cast<int>(rank) * (BN / 2);
-        for (int kb = 0; kb < kbs; ++kb, ++it) {
+        for (int kb = kb0; kb < kb1; ++kb, ++it) {
           const int s = it % C::STAGES;
           if (!mbar_wait(&S->empty[s], ((it / C::STAGES) & 1) ^ 1, abort_flag, g.timeout_ns, kSiteEmpty)) {
             ok = false;
@@ -448,7 +472,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
           const uint32_t sa = smem_u32(smem + s * C::STAGE), sb = sa + kABytes;
           // both CTAs' bytes complete on the barrier of CTA 0, which issues the MMAs
           if (rank == 0) mbar_arrive_expect_tx(&S->full[s], 2 * C::STAGE);
-          const uint32_t bar = map_to_rank(smem_u32(&S->full[s]), 0);
+          const uint32_t bar = map_to_rank(smem_u32(&S->full[s]), lead);
           if constexpr (A_MN) {
             tma_load_2d_pair(sa, ma, m0, k0, bar);
             tma_load_2d_pair(sa + 8192, ma, m0 + 64, k0, bar);
@@ -484,7 +508,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
         }
         tc_fence_after();
         const uint32_t d = tmem + a * BN;
-        for (int kb = 0; kb < kbs; ++kb, ++it) {
+        for (int kb = kb0; kb < kb1; ++kb, ++it) {
           const int s = it % C::STAGES;
           if (!mbar_wait(&S->full[s], (it / C::STAGES) & 1, abort_flag, g.timeout_ns, kSiteFull)) {
             ok = false;
@@ -495,10 +519,10 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
           const uint64_t da = operand_desc<A_MN>(sa), db = operand_desc<B_MN>(sa + kABytes);
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            umma_pair<KIND>(d, da + k * kDescStep<A_MN>, db + k * kDescStep<B_MN>, g.idesc, (kb | k) != 0);
-          umma_commit_pair(&S->empty[s]);
+            umma_pair<KIND>(d, da + k * kDescStep<A_MN>, db + k * kDescStep<B_MN>, g.idesc, kb != kb0 || k != 0);
+          umma_commit_pair(&S->empty[s], lead);
         }
-        if (ok) umma_commit_pair(&S->tfull[a]);
+        if (ok) umma_commit_pair(&S->tfull[a], lead);
       }
       if (!ok) {  // wait for the MMAs already issued
         asm volatile(
@@ -521,29 +545,79 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
       const int64_t row0 = int64_t(m) * kBM + rank * 128 + quarter * 32, row = row0 + lane;
       const int nrows = static_cast<int>(min(int64_t(32), max(int64_t(0), P.M - row0)));
       const bool row_ok = row < P.M;
-      if (!__all_sync(0xFFFFFFFFu, mbar_wait(&S->tfull[a], (n_tile >> 1) & 1, abort_flag,
-                                             g.timeout_ns, kSiteTmemFull)))
-        break;
+      const bool ok = __all_sync(0xFFFFFFFFu, mbar_wait(&S->tfull[a], (n_tile >> 1) & 1, abort_flag,
+                                                        g.timeout_ns, kSiteTmemFull));
+      if (!ok && g.split == 1) break;
       tc_fence_after();
       const uint32_t d = tmem + a * BN + (uint32_t(quarter * 32) << 16);
-      // this warp's half of the columns, 32 at a time; after the last tensor
-      // memory read the accumulators go back to the MMAs
-      constexpr int W = EPI == kGated ? BN / 4 : BN / 2;
+      // Shared tile: once every CTA's products are done, its stages' memory
+      // takes the other pairs' accumulators, slot (sending pair, chunk of the
+      // owner's, gate or up), as 8 x 128 rows of 16 bytes.  After a wait that
+      // ran out there is something to send all the same, for no owner to wait in vain.
+      const uint32_t parts = smem_u32(smem);
+      const int maxch = (NCH + g.split - 1) / g.split;
+      if (g.split > 1) {
+        cluster_sync();
+        for (int o = 0; o < g.split; ++o) {
+          if (o == static_cast<int>(pair)) continue;
+          const uint32_t to_bar = map_to_rank(smem_u32(&S->parts), 2 * o + rank);
+          const int o0 = NCH * o / g.split, o1 = NCH * (o + 1) / g.split;
 #pragma unroll 1
-      for (int c = 0; c < W; c += 32) {
-        const int lc = half * W + c;
+          for (int i = 2 * o0 * G + half; i < 2 * o1 * G; i += 2) {  // (chunk, gate or up) and half
+            const int ch = i / 2 / G, gi = i / 2 % G;
+            uint32_t v[32];
+            tmem_ld_32(d + gi * (BN / 2) + ch * 32, v);
+            const uint32_t slot = ((pair * maxch + ch - o0) * G + gi) * kPartBytes + (quarter * 32 + lane) * 16;
+            const uint32_t to = map_to_rank(parts + slot, 2 * o + rank);
+#pragma unroll
+            for (int c4 = 0; c4 < 4; ++c4) {
+              const int cc = half * 4 + c4;
+              if (half)
+                st_async_v4(to + cc * 2048, to_bar, v[16 + 4 * c4], v[17 + 4 * c4], v[18 + 4 * c4], v[19 + 4 * c4]);
+              else
+                st_async_v4(to + cc * 2048, to_bar, v[4 * c4], v[1 + 4 * c4], v[2 + 4 * c4], v[3 + 4 * c4]);
+            }
+          }
+        }
+        if (!__all_sync(0xFFFFFFFFu, mbar_wait_cluster(&S->parts, 0, abort_flag, 4 * g.timeout_ns, kSiteParts)) || !ok)
+          break;
+      }
+      auto add_parts = [&](int ch, int gi, uint32_t (&v)[32]) {
+#pragma unroll
+        for (int c4 = 0; c4 < 8; ++c4) {
+          uint4 own = make_uint4(v[4 * c4], v[4 * c4 + 1], v[4 * c4 + 2], v[4 * c4 + 3]), sum = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll 1
+          for (int r = 0; r < g.split; ++r) {
+            const uint4 w = r == static_cast<int>(pair)
+                                ? own
+                                : ld_shared_v4(parts + ((r * maxch + ch - chunk0) * G + gi) * kPartBytes + c4 * 2048 +
+                                               (quarter * 32 + lane) * 16);
+            if constexpr (KIND == kI8Kind) {
+              sum.x += w.x; sum.y += w.y; sum.z += w.z; sum.w += w.w;
+            } else {
+              sum.x = __float_as_uint(__uint_as_float(sum.x) + __uint_as_float(w.x));
+              sum.y = __float_as_uint(__uint_as_float(sum.y) + __uint_as_float(w.y));
+              sum.z = __float_as_uint(__uint_as_float(sum.z) + __uint_as_float(w.z));
+              sum.w = __float_as_uint(__uint_as_float(sum.w) + __uint_as_float(w.w));
+            }
+          }
+          v[4 * c4] = sum.x; v[4 * c4 + 1] = sum.y; v[4 * c4 + 2] = sum.z; v[4 * c4 + 3] = sum.w;
+        }
+      };
+      // this warp's chunks; after the last tensor memory read the accumulators
+      // go back to the MMAs
+#pragma unroll 1
+      for (int ch = chunk0 + half; ch < chunk1; ch += 2) {
+        const int lc = ch * 32;
         const int64_t col = int64_t(n) * (EPI == kGated ? BN / 2 : BN) + lc, left = P.N - col;
         const bool any = left > 0 && nrows > 0;
-        uint4 gh[4], uh[4], lo[4];
+        uint4 now[EPI == kDGate ? 12 : 1];
         if constexpr (EPI == kDGate) {
+          // read once, and not before much else has passed through L2
           if (any) {
-            const uint4* sv = reinterpret_cast<const uint4*>(g.saved + saved_block(row0, col, P.N)) + lane;
+            const uint4* from = reinterpret_cast<const uint4*>(g.saved + saved_block(row0, col, P.N)) + lane;
 #pragma unroll
-            for (int q4 = 0; q4 < 4; ++q4) {
-              gh[q4] = sv[q4 * 32];
-              uh[q4] = sv[(4 + q4) * 32];
-              lo[q4] = sv[(8 + q4) * 32];
-            }
+            for (int i = 0; i < 12; ++i) now[i] = __ldcs(from + i * 32);
           }
         }
         uint32_t x[32], x1[EPI == kGated ? 32 : 1];
@@ -551,25 +625,28 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
           tmem_ld_2x32(d + lc, d + BN / 2 + lc, x, x1);
         else
           tmem_ld_32(d + lc, x);
-        if (c + 32 >= W) {
+        if (ch + 2 >= chunk1) {
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(map_to_rank(smem_u32(&S->tempty[a]), 0));
+          if (lane == 0) mbar_arrive_cluster(map_to_rank(smem_u32(&S->tempty[a]), lead));
         }
         if (!any) continue;
+        if (g.split > 1) {
+          add_parts(ch, 0, x);
+          if constexpr (EPI == kGated) add_parts(ch, 1, x1);
+        }
         const int64_t at = row0 * P.N + col;
         uint32_t pk[16];
         if constexpr (EPI == kGated) {
           if (g.saved != nullptr) {
-            uint4* sv = reinterpret_cast<uint4*>(g.saved + saved_block(row0, col, P.N)) + lane;
-            auto hi = [](uint32_t e, uint32_t o) { return (e >> 16) | (o & 0xFFFF0000u); };
+            uint4* to = reinterpret_cast<uint4*>(g.saved + saved_block(row0, col, P.N)) + lane;
 #pragma unroll
             for (int q4 = 0; q4 < 4; ++q4) {
               const uint32_t *e = x + 8 * q4, *f = x1 + 8 * q4;
-              sv[q4 * 32] = make_uint4(hi(e[0], e[1]), hi(e[2], e[3]), hi(e[4], e[5]), hi(e[6], e[7]));
-              sv[(4 + q4) * 32] = make_uint4(hi(f[0], f[1]), hi(f[2], f[3]), hi(f[4], f[5]), hi(f[6], f[7]));
-              sv[(8 + q4) * 32] = make_uint4(saved_low(e[0], f[0], e[1], f[1]), saved_low(e[2], f[2], e[3], f[3]),
-                                             saved_low(e[4], f[4], e[5], f[5]), saved_low(e[6], f[6], e[7], f[7]));
+              __stcs(to + q4 * 32, make_uint4(saved_high(e[0], e[1]), saved_high(e[2], e[3]), saved_high(e[4], e[5]), saved_high(e[6], e[7])));
+              __stcs(to + (4 + q4) * 32, make_uint4(saved_high(f[0], f[1]), saved_high(f[2], f[3]), saved_high(f[4], f[5]), saved_high(f[6], f[7])));
+              __stcs(to + (8 + q4) * 32, make_uint4(saved_low(e[0], f[0], e[1], f[1]), saved_low(e[2], f[2], e[3], f[3]),
+                                             saved_low(e[4], f[4], e[5], f[5]), saved_low(e[6], f[6], e[7], f[7])));
             }
           }
 #pragma unroll
@@ -595,7 +672,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
           uint32_t pg[16];
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            const uint32_t hw = (&gh[i / 4].x)[i % 4], uw = (&uh[i / 4].x)[i % 4], lw = (&lo[i / 4].x)[i % 4];
+            const uint32_t hw = (&now[i / 4].x)[i % 4], uw = (&now[4 + i / 4].x)[i % 4], lw = (&now[8 + i / 4].x)[i % 4];
             float dg[2], du[2];
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
@@ -646,6 +723,10 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
         }
       }
     }
+  }
+  if (g.split > 1 && warp >= kEpiWarps) {  // the epilogue warps' barrier after the products
+    __syncwarp();
+    cluster_sync();
   }
   tc_fence_before();
   __syncwarp();

@@ -98,7 +98,6 @@ int check_norm_H(int64_t H) {
 constexpr int64_t kMaxDim = 65536;        // widths of the gated block
 constexpr int64_t kMaxInt8N = 1 << 20;    // channels of the int8 product
 constexpr int64_t kMaxInt8K = 131056;     // K * 128 * 128 < 2^31: the int32 sums cannot overflow
-constexpr int64_t kSmallMaxT = 128;       // tokens up to which the weights are the MMA's rows
 
 // Row-major matrix of `rows` rows of `cols` elements (1 or 2 bytes), boxes of
 // 128 bytes x box_rows, 128-byte swizzle; outside the matrix reads zero.
@@ -126,7 +125,7 @@ struct Operand {
 };
 
 template <int KIND, bool A_MN, bool B_MN, int EPI>
-auto pair_kernel(int bn) {
+auto pair_kernel(int bn) -> void (*)(const dense::Args) {
   return bn == 256 ? dense::pair_gemm_kernel<KIND, A_MN, B_MN, EPI, 256>
                    : dense::pair_gemm_kernel<KIND, A_MN, B_MN, EPI, 128>;
 }
@@ -134,7 +133,7 @@ auto pair_kernel(int bn) {
 // What one launch computes, before a kernel is chosen for it.
 struct Product {
   Operand a[dense::kMaxProb], b[dense::kMaxProb];
-  void* out[dense::kMaxProb];
+  void* out[dense::kMaxProb] = {};  // several products: NULL leaves one out (its size still counts for the shape)
   int nprob = 1, nseg = 1;
   int type = dense::kBF16;  // operand type, or kF32 outputs of int8
   const void* residual = nullptr;
@@ -156,39 +155,90 @@ void common_args(A* g, const Product& p) {
   g->timeout_ns = g_timeout_ns.load();
 }
 
+// launch_pdl with clusters of `cluster` CTAs.
+template <typename A>
+int launch_cluster(const char* what, void (*kernel)(A), unsigned grid, int threads, size_t smem, int cluster,
+                   cudaStream_t s, const A& args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args);
+  if (e != cudaSuccess) return cuda_fail(e, what);
+  return MOE_OK;
+}
+
 int64_t div_up(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-template <int KIND, bool A_MN, bool B_MN, int EPI>
-int launch_pair(const Product& p, int sms, cudaStream_t s) {
-  const int elem = KIND == dense::kI8Kind ? 1 : 2, ke = 128 / elem;
-  auto tiles_of = [&](int bn) {
-    int64_t n = 0;
+// Tile width and pairs per tile of a launch on CTA pairs, and its estimated
+// time in nanoseconds.
+struct PairShape {
+  int bn, split;
+  int64_t ns;
+};
+
+// The choice with the smallest estimate.  Measured at T = 96 .. 2048 tokens and
+// widths of 512 to 4096: a k-block takes a pair 300 ns (256 columns) or 290 ns
+// (128; both wait for L2), everything else 7.2 or 5.6 us, and sharing a tile
+// 2.2 us more, or 0.9 us and 0.6 us for each pair above two.  E.g. T = 256,
+// N = K = 4096 in int8: 16 tiles of 256 columns 16.8 us, shared by two pairs
+// 14.2, by four 24 (two rounds of clusters); 32 tiles of 128 columns 15.0,
+// shared by two 11.6.
+template <int EPI>
+PairShape pair_shape(const Product& p, int64_t kbs, const DeviceInfo& dev) {
+  PairShape best{256, 1, INT64_MAX};
+  for (const int bn : {256, 128}) {
+    int64_t tiles = 0;
     for (int i = 0; i < p.nprob; ++i)
-      n += div_up(p.a[i].outer(), dense::kBM) *
-           div_up(p.b[i].outer(), EPI == dense::kGated ? bn / 2 : bn);
-    return n;
-  };
-  // 256-column tiles feed the tensor cores best; with fewer of them than
-  // clusters, 128-column ones put more SMs to work
-  const int bn = tiles_of(256) >= sms / 2 ? 256 : 128;
+      tiles += div_up(p.a[i].outer(), dense::kBM) * div_up(p.b[i].outer(), EPI == dense::kGated ? bn / 2 : bn);
+    for (int split = 1; split <= dense::kMaxPairs; ++split) {
+      // a shared tile has a cluster to itself: one round of them (33, 22 or 15 on 148 SMs)
+      if (split > 1 && (tiles > dev.clusters[split] || kbs < 4 * split)) continue;
+      const int64_t rounds = split > 1 ? 1 : div_up(tiles, dev.sms / 2);
+      const int64_t share = split == 1 ? 0 : bn == 256 ? 2200 : 900 + 600 * (split - 2);
+      const int64_t ns = rounds * div_up(kbs, split) * (bn == 256 ? 300 : 290) + (bn == 256 ? 7200 : 5600) + share;
+      if (ns < best.ns) best = {bn, split, ns};
+    }
+  }
+  return best;
+}
+
+// k-blocks of a product, over its segments
+template <int KIND>
+int64_t all_kblocks(const Product& p) {
+  return div_up(p.a[0].k(), KIND == dense::kI8Kind ? 128 : 64) * p.nseg;
+}
+
+template <int KIND, bool A_MN, bool B_MN, int EPI>
+int launch_pair(const Product& p, const DeviceInfo& dev, cudaStream_t s) {
+  const int elem = KIND == dense::kI8Kind ? 1 : 2, ke = 128 / elem;
   dense::Args g{};
-  g.nprob = p.nprob;
   g.nseg = p.nseg;
   g.kblocks = static_cast<int>(div_up(p.a[0].k(), ke));
+  const PairShape shape = pair_shape<EPI>(p, all_kblocks<KIND>(p), dev);
+  const int bn = shape.bn;
+  g.split = shape.split;
   int64_t tiles = 0;
-  const int nmaps = p.nprob > 1 ? p.nprob : p.nseg;
-  for (int i = 0; i < nmaps; ++i) {
-    int rc = make_map(&g.a[i], p.a[i].p, p.a[i].rows, p.a[i].cols, elem, A_MN ? 64 : 128);
-    if (!rc) rc = make_map(&g.b[i], p.b[i].p, p.b[i].rows, p.b[i].cols, elem, B_MN ? 64 : bn / 2);
-    if (rc) return rc;
-  }
-  if (EPI == dense::kGated) {  // b[1]: the up weights
-    int rc = make_map(&g.b[1], p.b[1].p, p.b[1].rows, p.b[1].cols, elem, 64);
-    if (rc) return rc;
-  }
   g.vec = true;
-  for (int i = 0; i < p.nprob; ++i) {
-    dense::Problem& q = g.p[i];
+  g.nprob = 0;
+  for (int i = 0; i < std::max(p.nprob, p.nseg); ++i) {  // products, or segments of one
+    if (p.nprob > 1 && p.out[i] == nullptr) continue;
+    const int j = p.nprob > 1 ? g.nprob : i;
+    int rc = make_map(&g.a[j], p.a[i].p, p.a[i].rows, p.a[i].cols, elem, A_MN ? 64 : 128);
+    if (!rc) rc = make_map(&g.b[j], p.b[i].p, p.b[i].rows, p.b[i].cols, elem, B_MN ? 64 : bn / 2);
+    if (rc) return rc;
+    if (i >= p.nprob) continue;
+    dense::Problem& q = g.p[g.nprob++];
     q.M = p.a[i].outer();
     q.N = p.b[i].outer();
     q.mt = static_cast<int>(div_up(q.M, dense::kBM));
@@ -198,13 +248,17 @@ int launch_pair(const Product& p, int sms, cudaStream_t s) {
     tiles += int64_t(q.mt) * q.nt;
     g.vec = g.vec && (q.N * (p.type == dense::kF32 ? 4 : 2)) % 16 == 0;
   }
+  if (EPI == dense::kGated) {  // b[1]: the up weights
+    int rc = make_map(&g.b[1], p.b[1].p, p.b[1].rows, p.b[1].cols, elem, 64);
+    if (rc) return rc;
+  }
   g.tiles = static_cast<int>(tiles);
   common_args(&g, p);
   g.idesc = dense::make_idesc(KIND, p.type, A_MN, B_MN, dense::kBM, bn);
-  const unsigned grid = 2 * static_cast<unsigned>(std::min<int64_t>(tiles, sms / 2));
+  const int64_t clusters = g.split > 1 ? tiles : std::min<int64_t>(tiles, dev.sms / 2);
   const size_t smem = bn == 256 ? dense::PairCfg<256>::SMEM : dense::PairCfg<128>::SMEM;
-  return launch_pdl("pair_gemm_kernel launch", pair_kernel<KIND, A_MN, B_MN, EPI>(bn), dim3(grid),
-                    dim3(dense::kPairThreads), smem, s, g);
+  return launch_cluster("pair_gemm_kernel launch", pair_kernel<KIND, A_MN, B_MN, EPI>(bn),
+                        static_cast<unsigned>(clusters * 2 * g.split), dense::kPairThreads, smem, 2 * g.split, s, g);
 }
 
 template <int KIND, bool W_MN, int EPI, int NT, int ROWS>
@@ -234,23 +288,9 @@ int launch_small_rows(const Product& p, int sms, cudaStream_t s) {
   g.out = p.out[0];
   common_args(&g, p);
   g.idesc = dense::make_idesc(KIND, p.type, W_MN, false, 128, NT);
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(tiles * g.split));
-  cfg.blockDim = dim3(dense::kSmallThreads);
-  cfg.dynamicSmemBytes = dense::SmallCfg<NT, ROWS>::SMEM;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = static_cast<unsigned>(g.split);
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, dense::small_gemm_kernel<KIND, W_MN, EPI, NT, ROWS>, g);
-  if (e != cudaSuccess) return cuda_fail(e, "small_gemm_kernel launch");
-  return MOE_OK;
+  return launch_cluster("small_gemm_kernel launch", dense::small_gemm_kernel<KIND, W_MN, EPI, NT, ROWS>,
+                        static_cast<unsigned>(tiles * g.split), dense::kSmallThreads,
+                        dense::SmallCfg<NT, ROWS>::SMEM, g.split, s, g);
 }
 
 template <int KIND, bool W_MN, int EPI, int NT>
@@ -264,14 +304,21 @@ int launch_small_nt(const Product& p, int sms, cudaStream_t s) {
   return launch_small_rows<KIND, W_MN, EPI, NT, 128>(p, sms, s);
 }
 
+// One product of T tokens with weights.  Up to 32 tokens the weights are the
+// MMA's rows; above, by the estimate of both ways: with the weights as rows
+// 4.5 us and 0.5 us for each k-block (128 weight rows x 64 tokens) that an SM
+// gets, measured over the sizes that pair_shape names (T = 256, K = 1536,
+// int8: N = 512 4.7 us against 8.0 on pairs, N = 4096 10.9 against 8.7).
 template <int KIND, bool B_MN, int EPI>
-int launch_product(const Product& p, int sms, cudaStream_t s) {
+int launch_product(const Product& p, const DeviceInfo& dev, cudaStream_t s) {
   const int64_t T = p.a[0].outer();
-  if (T <= 16) return launch_small_nt<KIND, B_MN, EPI, 16>(p, sms, s);
-  if (T <= 32) return launch_small_nt<KIND, B_MN, EPI, 32>(p, sms, s);
-  if (T <= 64) return launch_small_nt<KIND, B_MN, EPI, 64>(p, sms, s);
-  if (T <= kSmallMaxT) return launch_small_nt<KIND, B_MN, EPI, 128>(p, sms, s);
-  return launch_pair<KIND, false, B_MN, EPI>(p, sms, s);
+  if (T <= 16) return launch_small_nt<KIND, B_MN, EPI, 16>(p, dev.sms, s);
+  if (T <= 32) return launch_small_nt<KIND, B_MN, EPI, 32>(p, dev.sms, s);
+  const int64_t tiles = div_up(p.b[0].outer(), EPI == dense::kGated ? 64 : 128) * div_up(T, 64);
+  const int64_t kbs = all_kblocks<KIND>(p);
+  if (4500 + tiles * kbs * 500 / dev.sms <= pair_shape<EPI>(p, kbs, dev).ns)
+    return launch_small_nt<KIND, B_MN, EPI, 64>(p, dev.sms, s);
+  return launch_pair<KIND, false, B_MN, EPI>(p, dev, s);
 }
 
 template <int KIND, bool A_MN, bool B_MN, int EPI>
@@ -298,10 +345,11 @@ cudaError_t small_attr() {
   cudaError_t e = small_attr_nt<KIND, W_MN, EPI, 16>();
   if (e == cudaSuccess) e = small_attr_nt<KIND, W_MN, EPI, 32>();
   if (e == cudaSuccess) e = small_attr_nt<KIND, W_MN, EPI, 64>();
-  if (e == cudaSuccess) e = small_attr_nt<KIND, W_MN, EPI, 128>();
   return e;
 }
-cudaError_t dense_attributes() {
+// Shared-memory limits of the kernels, and how many clusters of the pair
+// kernel the device runs at once.
+cudaError_t dense_setup(DeviceInfo* dev) {
   using namespace dense;
   cudaError_t e = pair_attr<kF16Kind, false, true, kGated>();
   if (e == cudaSuccess) e = pair_attr<kF16Kind, false, true, kPlain>();
@@ -314,6 +362,21 @@ cudaError_t dense_attributes() {
   if (e == cudaSuccess) e = small_attr<kF16Kind, false, kPlain>();
   if (e == cudaSuccess) e = small_attr<kF16Kind, false, kDGate>();
   if (e == cudaSuccess) e = small_attr<kI8Kind, false, kScaled>();
+  for (int split = 2; e == cudaSuccess && split <= kMaxPairs; ++split) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(2 * split));
+    cfg.blockDim = dim3(kPairThreads);
+    cfg.dynamicSmemBytes = PairCfg<256>::SMEM;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = static_cast<unsigned>(2 * split);
+    attr.val.clusterDim.y = 1;
+    attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    e = cudaOccupancyMaxActiveClusters(&dev->clusters[split],
+                                       pair_gemm_kernel<kF16Kind, false, true, kPlain, 256>, &cfg);
+  }
   return e;
 }
 
@@ -418,8 +481,8 @@ int moe_int8_matmul(const int8_t* a, const float* a_scale, const int8_t* b, cons
   REQUIRE(aligned(a, 16) && aligned(a_scale, 16) && aligned(b, 16) && aligned(b_scale, 16) && aligned(bias, 16) &&
               aligned(out, 16),
           "pointers must be 16-byte aligned");
-  int sms = 0;
-  rc = device_setup(nullptr, &sms);
+  DeviceInfo dev;
+  rc = device_info(&dev);
   if (rc) return rc;
   Product p{};
   p.a[0] = {a, T, K, false};
@@ -429,7 +492,7 @@ int moe_int8_matmul(const int8_t* a, const float* a_scale, const int8_t* b, cons
   p.a_scale = a_scale;
   p.b_scale = b_scale;
   p.bias = bias;
-  return launch_product<dense::kI8Kind, false, dense::kScaled>(p, sms, reinterpret_cast<cudaStream_t>(stream));
+  return launch_product<dense::kI8Kind, false, dense::kScaled>(p, dev, reinterpret_cast<cudaStream_t>(stream));
 }
 
 size_t moe_gated_ffn_saved_bytes(int64_t T, int64_t I) {
@@ -447,8 +510,8 @@ int moe_gated_ffn(const void* x, const void* w_gate, const void* w_up, const voi
   REQUIRE(aligned(x, 16) && aligned(w_gate, 16) && aligned(w_up, 16) && aligned(w_down, 16) && aligned(h, 16) &&
               aligned(saved, 16) && aligned(y, 16) && aligned(residual, 16),
           "pointers must be 16-byte aligned");
-  int sms = 0;
-  rc = device_setup(nullptr, &sms);
+  DeviceInfo dev;
+  rc = device_info(&dev);
   if (rc) return rc;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   Product up{};
@@ -458,7 +521,7 @@ int moe_gated_ffn(const void* x, const void* w_gate, const void* w_up, const voi
   up.out[0] = h;
   up.type = dtype;
   up.saved = saved;
-  rc = launch_product<dense::kF16Kind, true, dense::kGated>(up, sms, s);
+  rc = launch_product<dense::kF16Kind, true, dense::kGated>(up, dev, s);
   if (rc) return rc;
   Product down{};
   down.a[0] = {h, T, I, false};
@@ -467,7 +530,7 @@ int moe_gated_ffn(const void* x, const void* w_gate, const void* w_up, const voi
   down.type = dtype;
   down.residual = residual;
   down.early = true;
-  return launch_product<dense::kF16Kind, true, dense::kPlain>(down, sms, s);
+  return launch_product<dense::kF16Kind, true, dense::kPlain>(down, dev, s);
 }
 
 size_t moe_gated_ffn_backward_workspace_bytes(int64_t T, int64_t I) {
@@ -487,9 +550,9 @@ int moe_gated_ffn_backward(const void* dy, const void* x, const void* w_gate, co
           "pointers must be 16-byte aligned");
   void* dw[3] = {dw_gate, dw_up, dw_down};
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  int sms = 0;
+  DeviceInfo dev;
   if (T == 0) {  // the gradients of no tokens
-    rc = device_setup(nullptr, &sms);
+    rc = device_info(&dev);
     if (rc) return rc;
     for (void* d : dw)
       if (d) MOE_CUDA(cudaMemsetAsync(d, 0, static_cast<size_t>(H) * static_cast<size_t>(I) * 2, s), "cudaMemsetAsync");
@@ -503,7 +566,7 @@ int moe_gated_ffn_backward(const void* dy, const void* x, const void* w_gate, co
   if (need && (workspace == nullptr || workspace_bytes < need))
     return fail(MOE_ERR_WORKSPACE, "moe_gated_ffn_backward workspace needs %zu bytes, got %zu", need,
                 workspace ? workspace_bytes : size_t(0));
-  rc = device_setup(nullptr, &sms);
+  rc = device_info(&dev);
   if (rc) return rc;
   char* dg = static_cast<char*>(workspace);
   char* du = dg + static_cast<size_t>(T) * static_cast<size_t>(I) * 2;
@@ -515,7 +578,7 @@ int moe_gated_ffn_backward(const void* dy, const void* x, const void* w_gate, co
     p.out2 = du;
     p.type = dtype;
     p.saved = const_cast<void*>(saved);
-    rc = launch_product<dense::kF16Kind, false, dense::kDGate>(p, sms, s);
+    rc = launch_product<dense::kF16Kind, false, dense::kDGate>(p, dev, s);
     if (rc) return rc;
   }
   if (dx) {
@@ -528,27 +591,21 @@ int moe_gated_ffn_backward(const void* dy, const void* x, const void* w_gate, co
     p.early = true;
     p.out[0] = dx;
     p.type = dtype;
-    rc = launch_product<dense::kF16Kind, false, dense::kPlain>(p, sms, s);
+    rc = launch_product<dense::kF16Kind, false, dense::kPlain>(p, dev, s);
     if (rc) return rc;
   }
-  // the weights' gradients asked for, in one launch
+  // The weights' gradients asked for, in one launch, whose shape goes by all
+  // three: a gradient's bits do not depend on which others are wanted.
+  if (!dw_gate && !dw_up && !dw_down) return MOE_OK;
   Product p{};
-  p.nprob = 0;
+  p.nprob = 3;
   p.type = dtype;
   for (int i = 0; i < 3; ++i) {
-    if (!dw[i]) continue;
-    const int j = p.nprob++;
-    if (i < 2) {
-      p.a[j] = {x, T, H, true};
-      p.b[j] = {i == 0 ? dg : du, T, I, true};
-    } else {
-      p.a[j] = {h, T, I, true};
-      p.b[j] = {dy, T, H, true};
-    }
-    p.out[j] = dw[i];
+    p.a[i] = i < 2 ? Operand{x, T, H, true} : Operand{h, T, I, true};
+    p.b[i] = i < 2 ? Operand{i == 0 ? dg : du, T, I, true} : Operand{dy, T, H, true};
+    p.out[i] = dw[i];
   }
-  if (p.nprob == 0) return MOE_OK;
-  return launch_pair<dense::kF16Kind, true, true, dense::kPlain>(p, sms, s);
+  return launch_pair<dense::kF16Kind, true, true, dense::kPlain>(p, dev, s);
 }
 
 // ---- the pre-norm layer ------------------------------------------------------------

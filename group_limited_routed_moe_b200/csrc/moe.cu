@@ -78,7 +78,8 @@ bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) %
 // ---- per-device setup (once): SM count, arch check, kernel attributes -------
 struct DeviceInfo {
   int sms = 0;
-  int status = -1;  // -1 unset, otherwise moe_status
+  int clusters[5] = {};  // clusters of 2 * i CTAs, an SM each, that run at once
+  int status = -1;       // -1 unset, otherwise moe_status
   char msg[256] = "";
 };
 DeviceInfo g_dev[kMaxDevices];
@@ -86,7 +87,7 @@ std::mutex g_dev_mu;
 
 PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
 
-cudaError_t dense_attributes();  // shared-memory limits of the dense products' kernels
+cudaError_t dense_setup(DeviceInfo* dev);  // the dense products' kernels
 
 int device_setup(int* dev_out, int* sms_out) {
   int dev = 0;
@@ -136,7 +137,7 @@ int device_setup(int* dev_out, int* sms_out) {
       if (e == cudaSuccess)
         e = cudaFuncSetAttribute(router::router_kernel,
                                  cudaFuncAttributeMaxDynamicSharedMemorySize, router::SMEM_BYTES);
-      if (e == cudaSuccess) e = dense_attributes();
+      if (e == cudaSuccess) e = dense_setup(&d);
       if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute");
       if (g_encode == nullptr) {
         cudaDriverEntryPointQueryResult q;
@@ -152,6 +153,16 @@ int device_setup(int* dev_out, int* sms_out) {
   if (d.status != MOE_OK) return fail(d.status, "%s", d.msg);
   if (dev_out) *dev_out = dev;
   if (sms_out) *sms_out = d.sms;
+  return MOE_OK;
+}
+
+// A copy of the current device's record.
+int device_info(DeviceInfo* out) {
+  int dev = 0;
+  const int rc = device_setup(&dev, nullptr);
+  if (rc) return rc;
+  std::lock_guard<std::mutex> lk(g_dev_mu);
+  *out = g_dev[dev];
   return MOE_OK;
 }
 

@@ -795,30 +795,17 @@ def _leading(name: str, t: torch.Tensor, dtypes) -> tuple[torch.device, torch.dt
     return t.device, t.dtype
 
 
-class _on:
-    """Makes a tensor's device current, and on it the stream of the call, so
-    that what the call allocates belongs to that stream; enters with the raw
-    stream.  On the current device and stream, nothing has to be set."""
+_current_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
 
-    __slots__ = ("device", "stream", "guards")
 
-    def __init__(self, device, stream):
-        self.device, self.stream, self.guards = device, stream, ()
-
-    def __enter__(self):
-        if self.stream is not None:
-            if self.stream.device != self.device:
-                raise ValueError(f"stream on {self.stream.device}, tensors on {self.device}")
-            self.guards = (torch.cuda.stream(self.stream),)
-        elif torch.cuda.current_device() != self.device.index:
-            self.guards = (torch.cuda.device(self.device),)
-        for g in self.guards:
-            g.__enter__()
-        return torch._C._cuda_getCurrentRawStream(self.device.index)
-
-    def __exit__(self, *exc):
-        for g in self.guards:
-            g.__exit__(*exc)
+def _elsewhere(call, device, stream, *args, **kw):
+    """The call with `device` and, on it, `stream` made current (what the call
+    allocates then belongs to that stream): the way of every call whose tensors
+    are on another device than the current one, or that names a stream."""
+    if stream is not None and stream.device != device:
+        raise ValueError(f"stream on {stream.device}, tensors on {device}")
+    with torch.cuda.device(device), torch.cuda.stream(stream):
+        return call(*args, **kw)
 
 
 def _adr(t):
@@ -827,7 +814,7 @@ def _adr(t):
 
 def _new(name, t, shape, dtype, device):
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty(*shape, dtype=dtype, device=device)
     _expect(name, t, shape, dtype, device)
     return t
 
@@ -863,30 +850,34 @@ def moe_add_rmsnorm(x: torch.Tensor, residual: torch.Tensor | None = None, weigh
     None), int8 or float8_e4m3fn; scales fp32 [T, 1], or [T, ceil(H / 128)]
     with group = 128.  Without residual s is x."""
     dev, dt = _leading("x", x, _T16)
-    if out_format not in NORM_FORMATS:
+    if stream is not None or _current_device() != dev.index:
+        return _elsewhere(moe_add_rmsnorm, dev, stream, x, residual, weight, eps, out_format, group, stream_out,
+                          out, scales)
+    fmt = NORM_FORMATS.get(out_format)
+    if fmt is None:
         raise ValueError(f"out_format {out_format!r}: one of {sorted(NORM_FORMATS)}")
-    fmt = NORM_FORMATS[out_format]
-    if group not in (0, NORM_GROUP) or (group and not fmt):
+    if group and (group != NORM_GROUP or not fmt):
         raise ValueError(f"group {group}: 0, or {NORM_GROUP} with an 8-bit format")
     T, H = x.shape
-    if residual is not None:
-        _expect("residual", residual, x.shape, dt, dev)
     if weight is not None:
         _expect("weight", weight, (H,), dt, dev)
-    with _on(dev, stream) as s:
-        if residual is None:
-            stream_out = x
-        else:
-            stream_out = _new_like("stream_out", stream_out, x)
-        if fmt:
-            out = _new("out", out, x.shape, torch.int8 if fmt == 1 else torch.float8_e4m3fn, dev)
-            scales = _new("scales", scales, (T, -(-H // group) if group else 1), torch.float32, dev)
-        else:
-            out = _new_like("out", out, x)
-            scales = None
-        _check("moe_add_rmsnorm", lib.moe_add_rmsnorm(
-            _adr(x), _adr(residual), _adr(weight), eps, T, H, _TYPES[dt],
-            None if residual is None else _adr(stream_out), fmt, group, _adr(out), _adr(scales), s))
+    s_ptr = None
+    if residual is None:
+        stream_out = x
+    else:
+        _expect("residual", residual, (T, H), dt, dev)
+        stream_out = _new_like("stream_out", stream_out, x)
+        s_ptr = stream_out.data_ptr()
+    if fmt:
+        out = _new("out", out, (T, H), torch.int8 if fmt == 1 else torch.float8_e4m3fn, dev)
+        scales = _new("scales", scales, (T, -(-H // group) if group else 1), torch.float32, dev)
+    else:
+        out = _new_like("out", out, x)
+        scales = None
+    rc = lib.moe_add_rmsnorm(x.data_ptr(), _adr(residual), _adr(weight), eps, T, H, _TYPES[dt], s_ptr, fmt, group,
+                             out.data_ptr(), _adr(scales), _raw_stream(dev.index))
+    if rc:
+        _check("moe_add_rmsnorm", rc)
     return stream_out, out, scales
 
 
@@ -895,23 +886,26 @@ def moe_add_rmsnorm_backward(dy: torch.Tensor, s: torch.Tensor, weight=None, eps
     """Gradients of moe_add_rmsnorm's 16-bit form: (dx [T, H], dweight [H] fp32
     or None); dx is the gradient of x and of residual (see include/moe.h)."""
     dev, dt = _leading("dy", dy, _T16)
+    if stream is not None or _current_device() != dev.index:
+        return _elsewhere(moe_add_rmsnorm_backward, dev, stream, dy, s, weight, eps, dstream, dx, dweight,
+                          need_dweight, workspace)
     T, H = dy.shape
-    _expect("s", s, dy.shape, dt, dev)
+    _expect("s", s, (T, H), dt, dev)
     if weight is not None:
         _expect("weight", weight, (H,), dt, dev)
     if dstream is not None:
-        _expect("dstream", dstream, dy.shape, dt, dev)
-    with _on(dev, stream) as st:
-        dx = _new_like("dx", dx, dy)
-        if need_dweight:
-            dweight = _new("dweight", dweight, (H,), torch.float32, dev)
-            workspace = _scratch("workspace", workspace,
-                                 int(lib.moe_add_rmsnorm_backward_workspace_bytes(T, H)), dev)
-        else:
-            dweight = workspace = None
-        _check("moe_add_rmsnorm_backward", lib.moe_add_rmsnorm_backward(
-            _adr(dy), _adr(s), _adr(weight), eps, T, H, _TYPES[dt], _adr(dstream), _adr(dx), _adr(dweight),
-            _adr(workspace), _nbytes(workspace), st))
+        _expect("dstream", dstream, (T, H), dt, dev)
+    dx = _new_like("dx", dx, dy)
+    if need_dweight:
+        dweight = _new("dweight", dweight, (H,), torch.float32, dev)
+        workspace = _scratch("workspace", workspace, lib.moe_add_rmsnorm_backward_workspace_bytes(T, H), dev)
+    else:
+        dweight = workspace = None
+    rc = lib.moe_add_rmsnorm_backward(dy.data_ptr(), s.data_ptr(), _adr(weight), eps, T, H, _TYPES[dt],
+                                      _adr(dstream), dx.data_ptr(), _adr(dweight), _adr(workspace),
+                                      _nbytes(workspace), _raw_stream(dev.index))
+    if rc:
+        _check("moe_add_rmsnorm_backward", rc)
     return dx, dweight
 
 
@@ -919,34 +913,37 @@ def moe_int8_matmul(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor, b_s
                     bias=None, out_dtype: torch.dtype = torch.bfloat16, out=None, stream=None):
     """[T, N] = (a [T, K] int8 @ b [N, K] int8 transposed) * a_scale [T] (or
     [T, 1]) * b_scale [N] + bias [N] (see include/moe.h)."""
-    dev, _ = _leading("a", a, (torch.int8,))
+    dev, i8 = _leading("a", a, (torch.int8,))
+    if stream is not None or _current_device() != dev.index:
+        return _elsewhere(moe_int8_matmul, dev, stream, a, a_scale, b, b_scale, bias, out_dtype, out)
     if not isinstance(b, torch.Tensor) or b.dim() != 2:
         raise ValueError("b: expected a matrix [N, K]")
     T, K = a.shape
     N = b.shape[0]
-    _expect("b", b, (N, K), torch.int8, dev)
+    _expect("b", b, (N, K), i8, dev)
     _expect("a_scale", a_scale, (T, 1) if a_scale.dim() == 2 else (T,), torch.float32, dev)
     _expect("b_scale", b_scale, (N,), torch.float32, dev)
     if bias is not None:
         _expect("bias", bias, (N,), torch.float32, dev)
     if out_dtype not in _TYPES:
         raise ValueError(f"out_dtype {out_dtype}: bf16, fp16 or fp32")
-    with _on(dev, stream) as s:
-        out = _new("out", out, (T, N), out_dtype, dev)
-        _check("moe_int8_matmul", lib.moe_int8_matmul(
-            _adr(a), _adr(a_scale), _adr(b), _adr(b_scale), _adr(bias), T, N, K, _TYPES[out_dtype], _adr(out), s))
+    out = _new("out", out, (T, N), out_dtype, dev)
+    rc = lib.moe_int8_matmul(a.data_ptr(), a_scale.data_ptr(), b.data_ptr(), b_scale.data_ptr(), _adr(bias), T, N, K,
+                             _TYPES[out_dtype], out.data_ptr(), _raw_stream(dev.index))
+    if rc:
+        _check("moe_int8_matmul", rc)
     return out
 
 
-def _ffn_shapes(x, w_gate, w_up, w_down):
-    dev, dt = _leading("x", x, _T16)
+def _ffn_shapes(x, w_gate, w_up, w_down, dev, dt):
     T, H = x.shape
     if not isinstance(w_gate, torch.Tensor) or w_gate.dim() != 2:
         raise ValueError("w_gate: expected a matrix [H, I]")
     I = w_gate.shape[1]
-    for name, w, shape in (("w_gate", w_gate, (H, I)), ("w_up", w_up, (H, I)), ("w_down", w_down, (I, H))):
-        _expect(name, w, shape, dt, dev)
-    return dev, dt, T, H, I
+    _expect("w_gate", w_gate, (H, I), dt, dev)
+    _expect("w_up", w_up, (H, I), dt, dev)
+    _expect("w_down", w_down, (I, H), dt, dev)
+    return T, H, I
 
 
 def moe_gated_ffn(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, w_down: torch.Tensor,
@@ -955,16 +952,19 @@ def moe_gated_ffn(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, w_d
     x [T, H], w_gate and w_up [H, I], w_down [I, H] of one 16-bit type (see
     include/moe.h).  Returns y, or with save = True (y, saved): what
     moe_gated_ffn_backward needs of this call."""
-    dev, dt, T, H, I = _ffn_shapes(x, w_gate, w_up, w_down)
+    dev, dt = _leading("x", x, _T16)
+    if stream is not None or _current_device() != dev.index:
+        return _elsewhere(moe_gated_ffn, dev, stream, x, w_gate, w_up, w_down, residual, save, h, y)
+    T, H, I = _ffn_shapes(x, w_gate, w_up, w_down, dev, dt)
     if residual is not None:
         _expect("residual", residual, (T, H), dt, dev)
-    with _on(dev, stream) as s:
-        h = _new("h", h, (T, I), dt, dev)
-        y = _new_like("y", y, x)
-        pre = torch.empty(int(lib.moe_gated_ffn_saved_bytes(T, I)), dtype=torch.uint8, device=dev) if save else None
-        _check("moe_gated_ffn", lib.moe_gated_ffn(
-            _adr(x), _adr(w_gate), _adr(w_up), _adr(w_down), T, H, I, _TYPES[dt], _adr(residual), _adr(h),
-            _adr(pre), _adr(y), s))
+    h = _new("h", h, (T, I), dt, dev)
+    y = _new_like("y", y, x)
+    pre = torch.empty(lib.moe_gated_ffn_saved_bytes(T, I), dtype=torch.uint8, device=dev) if save else None
+    rc = lib.moe_gated_ffn(x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(), w_down.data_ptr(), T, H, I, _TYPES[dt],
+                           _adr(residual), h.data_ptr(), _adr(pre), y.data_ptr(), _raw_stream(dev.index))
+    if rc:
+        _check("moe_gated_ffn", rc)
     return (y, (h, pre)) if save else y
 
 
@@ -974,25 +974,32 @@ def moe_gated_ffn_backward(dy: torch.Tensor, x: torch.Tensor, w_gate: torch.Tens
     """Gradients of moe_gated_ffn: (dx, dw_gate, dw_up, dw_down) in the inputs'
     type, None where `need` is false; `saved` from the forward call with
     save = True.  The residual's gradient is dy."""
-    dev, dt, T, H, I = _ffn_shapes(x, w_gate, w_up, w_down)
-    _expect("dy", dy, (T, H), dt, dev)
+    dev, dt = _leading("dy", dy, _T16)
+    if stream is not None or _current_device() != dev.index:
+        return _elsewhere(moe_gated_ffn_backward, dev, stream, dy, x, w_gate, w_up, w_down, saved, need, dx, dw_gate,
+                          dw_up, dw_down, workspace)
+    if len(need) != 4:
+        raise ValueError("need: one truth value for each of dx, dw_gate, dw_up, dw_down")
+    T, H, I = _ffn_shapes(dy, w_gate, w_up, w_down, dev, dt)
+    _expect("x", x, (T, H), dt, dev)
     h, pre = saved
     _expect("saved h", h, (T, I), dt, dev)
-    _expect("saved pre-activations", pre, (int(lib.moe_gated_ffn_saved_bytes(T, I)),), torch.uint8, dev)
-    with _on(dev, stream) as s:
-        outs = [_new(name, t, shape, dt, dev) if want else None
-                for want, name, t, shape in zip(need, ("dx", "dw_gate", "dw_up", "dw_down"),
-                                                (dx, dw_gate, dw_up, dw_down),
-                                                ((T, H), (H, I), (H, I), (I, H)), strict=True)]
-        if any(need[:3]):
-            workspace = _scratch("workspace", workspace,
-                                 int(lib.moe_gated_ffn_backward_workspace_bytes(T, I)), dev)
-        else:
-            workspace = None
-        _check("moe_gated_ffn_backward", lib.moe_gated_ffn_backward(
-            _adr(dy), _adr(x), _adr(w_gate), _adr(w_up), _adr(w_down), _adr(h), _adr(pre), T, H, I, _TYPES[dt],
-            *(_adr(t) for t in outs), _adr(workspace), _nbytes(workspace), s))
-    return tuple(outs)
+    _expect("saved pre-activations", pre, (lib.moe_gated_ffn_saved_bytes(T, I),), torch.uint8, dev)
+    dx = _new_like("dx", dx, dy) if need[0] else None
+    dw_gate = _new_like("dw_gate", dw_gate, w_gate) if need[1] else None
+    dw_up = _new_like("dw_up", dw_up, w_up) if need[2] else None
+    dw_down = _new_like("dw_down", dw_down, w_down) if need[3] else None
+    if need[0] or need[1] or need[2]:
+        workspace = _scratch("workspace", workspace, lib.moe_gated_ffn_backward_workspace_bytes(T, I), dev)
+    else:
+        workspace = None
+    rc = lib.moe_gated_ffn_backward(dy.data_ptr(), x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(),
+                                    w_down.data_ptr(), h.data_ptr(), pre.data_ptr(), T, H, I, _TYPES[dt], _adr(dx),
+                                    _adr(dw_gate), _adr(dw_up), _adr(dw_down), _adr(workspace), _nbytes(workspace),
+                                    _raw_stream(dev.index))
+    if rc:
+        _check("moe_gated_ffn_backward", rc)
+    return dx, dw_gate, dw_up, dw_down
 
 
 def layer_normed_workspace_bytes(T: int) -> int:
@@ -1011,28 +1018,36 @@ def moe_layer_normed(x: torch.Tensor, residual, norm_weight, eps: float, packed_
                      workspace: torch.Tensor | None = None, stream=None):
     """The routed layer with its norm in front (see include/moe.h): returns
     (s, out) with s = round(x + residual), out = round(s + MoE(RMSNorm(s)))."""
-    dev, _ = _leading("x", x, (torch.bfloat16,))
+    dev, dt = _leading("x", x, (torch.bfloat16,))
+    if stream is not None or _current_device() != dev.index:
+        return _elsewhere(moe_layer_normed, dev, stream, x, residual, norm_weight, eps, packed_router, bias, packed_w,
+                          stream_out, out, topk_idx_out, topk_w_out, workspace)
     T = x.shape[0]
-    _expect("x", x, (T, HIDDEN), torch.bfloat16, dev)
-    for name, t, shape, dt in (("residual", residual, (T, HIDDEN), torch.bfloat16),
-                               ("norm_weight", norm_weight, (HIDDEN,), torch.bfloat16),
+    _expect("x", x, (T, HIDDEN), dt, dev)
+    for name, t, shape, ty in (("residual", residual, (T, HIDDEN), dt), ("norm_weight", norm_weight, (HIDDEN,), dt),
                                ("bias", bias, (N_EXPERTS,), torch.float32),
                                ("topk_idx_out", topk_idx_out, (T, TOPK), torch.int32),
                                ("topk_w_out", topk_w_out, (T, TOPK), torch.float32)):
         if t is not None:
-            _expect(name, t, shape, dt, dev)
-    with _on(dev, stream) as s:
-        if residual is None:
-            stream_out = x
-        else:
-            stream_out = _new("stream_out", stream_out, x.shape, torch.bfloat16, dev)
-        out = _new("out", out, x.shape, torch.bfloat16, dev)
-        if workspace is None:
-            workspace = alloc_layer_normed_workspace(T, dev)
-        _check("moe_layer_normed", lib.moe_layer_normed(
-            _adr(x), _adr(residual), _adr(norm_weight), eps, _adr(packed_router), _adr(bias), _adr(packed_w), T,
-            None if residual is None else _adr(stream_out), _adr(out), _adr(topk_idx_out), _adr(topk_w_out),
-            _adr(workspace), _nbytes(workspace), s))
+            _expect(name, t, shape, ty, dev)
+    for name, t, n in (("packed_router", packed_router, lib.moe_router_packed_bytes()),
+                       ("packed_w", packed_w, lib.moe_packed_weight_bytes())):
+        if not isinstance(t, torch.Tensor) or t.device != dev or not t.is_contiguous() or _nbytes(t) != n:
+            raise ValueError(f"{name}: expected {n} contiguous bytes on {dev}")
+    s_ptr = None
+    if residual is None:
+        stream_out = x
+    else:
+        stream_out = _new_like("stream_out", stream_out, x)
+        s_ptr = stream_out.data_ptr()
+    out = _new_like("out", out, x)
+    if workspace is None:
+        workspace = alloc_layer_normed_workspace(T, dev)
+    rc = lib.moe_layer_normed(x.data_ptr(), _adr(residual), _adr(norm_weight), eps, packed_router.data_ptr(),
+                              _adr(bias), packed_w.data_ptr(), T, s_ptr, out.data_ptr(), _adr(topk_idx_out),
+                              _adr(topk_w_out), workspace.data_ptr(), _nbytes(workspace), _raw_stream(dev.index))
+    if rc:
+        _check("moe_layer_normed", rc)
     return stream_out, out
 
 

@@ -37,7 +37,8 @@ def _acc(K):
 
 INT8_SHAPES = [(1, 1, 16), (1, 8192, 1536), (2, 129, 16), (5, 64, 4096), (16, 1531, 1008), (17, 300, 144),
                (33, 1000, 272), (64, 128, 128), (65, 257, 1536), (128, 130, 640), (129, 127, 48), (200, 1531, 1008),
-               (256, 256, 128), (257, 513, 144), (1000, 1536, 512), (700, 4104, 400), (2500, 2000, 1536)]
+               (256, 256, 128), (257, 513, 144), (1000, 1536, 512), (700, 4104, 400), (2500, 2000, 1536),
+               (300, 1531, 4096), (700, 520, 2064), (257, 200, 3200), (1500, 264, 1280)]
 
 
 def _int8_inputs(T, N, K, seed):
@@ -176,7 +177,8 @@ def _ok(got, want, tol, what=""):
 
 FFN_SHAPES = [(1, 8, 8), (1, 1536, 512), (1, 72, 4104), (2, 136, 64), (15, 512, 136), (16, 256, 264), (17, 64, 1032),
               (40, 520, 1048), (64, 128, 128), (100, 328, 200), (128, 264, 72), (129, 64, 64), (200, 136, 520),
-              (256, 256, 256), (300, 392, 264), (515, 1000, 136), (1100, 264, 648)]
+              (256, 256, 256), (300, 392, 264), (515, 1000, 136), (1100, 264, 648),
+              (300, 1536, 520), (1000, 520, 2056), (257, 1032, 1544)]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
