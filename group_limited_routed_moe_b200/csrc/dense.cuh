@@ -127,8 +127,10 @@ __device__ __forceinline__ uint32_t map_to_rank(uint32_t addr, uint32_t rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
   return r;
 }
+// Arrives on a barrier of the cluster.  It orders no stores to global memory
+// for the other CTA (released at cluster scope it waited 1300 cycles for them).
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
 // Stores 16 bytes into the shared memory of a CTA of the cluster and completes
 // them on a barrier there.
@@ -302,12 +304,13 @@ __device__ __forceinline__ void tmem_ld_32(uint32_t taddr, uint32_t (&a)[32]) {
 
 // ---------------------------------------------------------------- block stores
 
-constexpr int kStageRow = 80;                  // padded 64-byte row
+constexpr int kStageRow = 64;
 constexpr int kStageWarp = 32 * kStageRow;     // one warp's block
 
 // Stores a warp's block of 32 rows x 64 bytes (lane = row, its 16 words in pk)
-// at g0 (row 0, first column): through the warp's padded shared tile, so that
-// each row leaves as one 64-byte segment.  nrows rows and `ncols` columns
+// at g0 (row 0, first column): through the warp's shared tile (16-byte pieces of
+// a row swapped by its number, which keeps both sides free of bank conflicts),
+// so that each row leaves as one 64-byte segment.  nrows rows and `ncols` columns
 // (elements of ES bytes) of it exist.  Rows that are not 16-byte aligned go
 // out element by element, lanes along the row.
 template <int ES, bool ALWAYS_VEC>
@@ -317,16 +320,19 @@ __device__ __forceinline__ void store_block(const uint32_t* pk, uint32_t stage, 
   const uint32_t mine = stage + lane * kStageRow;
 #pragma unroll
   for (int q = 0; q < 4; ++q)
-    st_shared_v4(mine + q * 16, pk[4 * q], pk[4 * q + 1], pk[4 * q + 2], pk[4 * q + 3]);
+    st_shared_v4(mine + ((q ^ (lane >> 1 & 3)) * 16), pk[4 * q], pk[4 * q + 1], pk[4 * q + 2], pk[4 * q + 3]);
   __syncwarp();
   if (ALWAYS_VEC || vec) {
+    const int row = lane >> 2, ch = lane & 3;  // and rows 8, 16, 24 further on
+    const uint32_t from = stage + row * kStageRow + ((ch ^ (row >> 1 & 3)) * 16);
+    uint8_t* to = g0 + row * ld_bytes + ch * 16;
+    const bool col_ok = (ch + 1) * (16 / ES) <= ncols;
+    uint4 v[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int row = i * 8 + (lane >> 2), ch = lane & 3;
-      const uint4 v = ld_shared_v4(stage + row * kStageRow + ch * 16);
-      if (row < nrows && (ch + 1) * (16 / ES) <= ncols)
-        st_global_v4(g0 + row * ld_bytes + ch * 16, v.x, v.y, v.z, v.w);
-    }
+    for (int i = 0; i < 4; ++i) v[i] = ld_shared_v4(from + i * 8 * kStageRow);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (col_ok && row + i * 8 < nrows) st_global_v4(to + i * 8 * ld_bytes, v[i].x, v[i].y, v[i].z, v[i].w);
   } else {
     constexpr int PER = 64 / ES;               // elements of a row: 32 or 16
     const int col = lane % PER;
@@ -334,11 +340,17 @@ __device__ __forceinline__ void store_block(const uint32_t* pk, uint32_t stage, 
       if (col < ncols) {
         if constexpr (ES == 2) {
           uint16_t v;
-          asm volatile("ld.shared.b16 %0, [%1];" : "=h"(v) : "r"(stage + r * kStageRow + col * 2) : "memory");
+          asm volatile("ld.shared.b16 %0, [%1];"
+                       : "=h"(v)
+                       : "r"(stage + r * kStageRow + ((col / 8 ^ (r >> 1 & 3)) * 16) + col % 8 * 2)
+                       : "memory");
           *reinterpret_cast<uint16_t*>(g0 + r * ld_bytes + col * 2) = v;
         } else {
           uint32_t v;
-          asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(stage + r * kStageRow + col * 4) : "memory");
+          asm volatile("ld.shared.b32 %0, [%1];"
+                       : "=r"(v)
+                       : "r"(stage + r * kStageRow + ((col / 4 ^ (r >> 1 & 3)) * 16) + col % 4 * 4)
+                       : "memory");
           *reinterpret_cast<uint32_t*>(g0 + r * ld_bytes + col * 4) = v;
         }
       }
@@ -362,7 +374,10 @@ __device__ __forceinline__ void load_row32(const uint16_t* p, bool row_ok, int64
 // ---------------------------------------------------------------- the pair kernel
 
 constexpr int kBM = 256;          // tile rows (128 per CTA)
-constexpr int kEpiWarps = 8;      // two per 32-lane quarter of tensor memory, a half of the columns each
+// Two epilogue warps per 32-lane quarter of tensor memory, taking its 32-column
+// chunks in turn.  (12 and 16 warps, with 128 and 96 registers a thread, made
+// the int8 product 2% faster and the gated one 3 to 10% slower at T = 8189.)
+constexpr int kEpiWarps = 8;
 constexpr int kPairThreads = 32 * (kEpiWarps + 2);
 constexpr int kABytes = 128 * kKB;
 constexpr int kPartBytes = 8 * 128 * 16;  // 32 accumulator columns of 128 rows
@@ -534,7 +549,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     }
   } else {
     // ---------------------------------------------- epilogue
-    const int quarter = warp & 3, half = warp >> 2;
+    const int quarter = warp & 3, sub = warp >> 2;
     const uint32_t stage = smem_u32(sEpi + warp * kStageWarp);
     int n_tile = 0;
     for (int t = cluster; t < g.tiles; t += nclusters, ++n_tile) {
@@ -545,6 +560,19 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       const int64_t row0 = int64_t(m) * kBM + rank * 128 + quarter * 32, row = row0 + lane;
       const int nrows = static_cast<int>(min(int64_t(32), max(int64_t(0), P.M - row0)));
       const bool row_ok = row < P.M;
+      // kScaled: the row's scale, and the scale and bias of one column of the
+      // warp's next chunk in each lane
+      float sa = 0.f, sb = 0.f, bi = 0.f;
+      auto column_scales = [&](int ch) {
+        const int64_t c = int64_t(n) * BN + ch * 32 + lane;
+        const bool in = ch < chunk1 && c < P.N;
+        sb = in ? g.b_scale[c] : 0.f;
+        bi = in && g.bias != nullptr ? g.bias[c] : 0.f;
+      };
+      if constexpr (EPI == kScaled) {
+        if (row_ok) sa = g.a_scale[row];
+        column_scales(chunk0 + sub);
+      }
       const bool ok = __all_sync(0xFFFFFFFFu, mbar_wait(&S->tfull[a], (n_tile >> 1) & 1, abort_flag,
                                                         g.timeout_ns, kSiteTmemFull));
       if (!ok && g.split == 1) break;
@@ -563,20 +591,15 @@ __global__ void __launch_bounds__(kPairThreads, 1)
           const uint32_t to_bar = map_to_rank(smem_u32(&S->parts), 2 * o + rank);
           const int o0 = NCH * o / g.split, o1 = NCH * (o + 1) / g.split;
 #pragma unroll 1
-          for (int i = 2 * o0 * G + half; i < 2 * o1 * G; i += 2) {  // (chunk, gate or up) and half
-            const int ch = i / 2 / G, gi = i / 2 % G;
+          for (int i = o0 * G + sub; i < o1 * G; i += kEpiWarps / 4) {
+            const int ch = i / G, gi = i % G;
             uint32_t v[32];
             tmem_ld_32(d + gi * (BN / 2) + ch * 32, v);
             const uint32_t slot = ((pair * maxch + ch - o0) * G + gi) * kPartBytes + (quarter * 32 + lane) * 16;
             const uint32_t to = map_to_rank(parts + slot, 2 * o + rank);
 #pragma unroll
-            for (int c4 = 0; c4 < 4; ++c4) {
-              const int cc = half * 4 + c4;
-              if (half)
-                st_async_v4(to + cc * 2048, to_bar, v[16 + 4 * c4], v[17 + 4 * c4], v[18 + 4 * c4], v[19 + 4 * c4]);
-              else
-                st_async_v4(to + cc * 2048, to_bar, v[4 * c4], v[1 + 4 * c4], v[2 + 4 * c4], v[3 + 4 * c4]);
-            }
+            for (int c4 = 0; c4 < 8; ++c4)
+              st_async_v4(to + c4 * 2048, to_bar, v[4 * c4], v[4 * c4 + 1], v[4 * c4 + 2], v[4 * c4 + 3]);
           }
         }
         if (!__all_sync(0xFFFFFFFFu, mbar_wait_cluster(&S->parts, 0, abort_flag, 4 * g.timeout_ns, kSiteParts)) || !ok)
@@ -604,10 +627,16 @@ __global__ void __launch_bounds__(kPairThreads, 1)
           v[4 * c4] = sum.x; v[4 * c4 + 1] = sum.y; v[4 * c4 + 2] = sum.z; v[4 * c4 + 3] = sum.w;
         }
       };
-      // this warp's chunks; after the last tensor memory read the accumulators
+      // this warp's chunks; after its last tensor memory read the accumulators
       // go back to the MMAs
+      auto release = [&] {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(map_to_rank(smem_u32(&S->tempty[a]), lead));
+      };
+      if (chunk0 + sub >= chunk1) release();
 #pragma unroll 1
-      for (int ch = chunk0 + half; ch < chunk1; ch += 2) {
+      for (int ch = chunk0 + sub; ch < chunk1; ch += kEpiWarps / 4) {
         const int lc = ch * 32;
         const int64_t col = int64_t(n) * (EPI == kGated ? BN / 2 : BN) + lc, left = P.N - col;
         const bool any = left > 0 && nrows > 0;
@@ -625,11 +654,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
           tmem_ld_2x32(d + lc, d + BN / 2 + lc, x, x1);
         else
           tmem_ld_32(d + lc, x);
-        if (ch + 2 >= chunk1) {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(map_to_rank(smem_u32(&S->tempty[a]), lead));
-        }
+        if (ch + kEpiWarps / 4 >= chunk1) release();
         if (!any) continue;
         if (g.split > 1) {
           add_parts(ch, 0, x);
@@ -686,28 +711,22 @@ __global__ void __launch_bounds__(kPairThreads, 1)
           store_block<2, true>(pg, stage, static_cast<uint8_t*>(P.out) + at * 2, P.N * 2, nrows, left, true, lane);
           store_block<2, true>(pk, stage, static_cast<uint8_t*>(g.out2) + at * 2, P.N * 2, nrows, left, true, lane);
         } else {
-          const float sa = row_ok ? g.a_scale[row] : 0.f;
-          if (left >= 32) {  // the scales of 32 columns, the same for every lane
+          // the 32 columns' values to every lane, through the warp's shared tile
+          asm volatile("st.shared.f32 [%0], %1;" ::"r"(stage + lane * 4), "f"(sb) : "memory");
+          asm volatile("st.shared.f32 [%0], %1;" ::"r"(stage + 128 + lane * 4), "f"(bi) : "memory");
+          __syncwarp();
+          column_scales(ch + kEpiWarps / 4);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const float4 sb = *reinterpret_cast<const float4*>(g.b_scale + col + 4 * i);
-              float4 bi = make_float4(0.f, 0.f, 0.f, 0.f);
-              if (g.bias != nullptr) bi = *reinterpret_cast<const float4*>(g.bias + col + 4 * i);
+          for (int i = 0; i < 8; ++i) {
+            const uint4 s4 = ld_shared_v4(stage + i * 16), b4 = ld_shared_v4(stage + 128 + i * 16);
 #pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                uint32_t& v = x[4 * i + j];
-                v = __float_as_uint(fmaf(static_cast<float>(static_cast<int>(v)) * sa, (&sb.x)[j], (&bi.x)[j]));
-              }
-            }
-          } else {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              const bool in = i < left;
-              const float sb = in ? g.b_scale[col + i] : 0.f;
-              const float bi = in && g.bias != nullptr ? g.bias[col + i] : 0.f;
-              x[i] = __float_as_uint(fmaf(static_cast<float>(static_cast<int>(x[i])) * sa, sb, bi));
+            for (int j = 0; j < 4; ++j) {
+              uint32_t& v = x[4 * i + j];
+              v = __float_as_uint(fmaf(static_cast<float>(static_cast<int>(v)) * sa, __uint_as_float((&s4.x)[j]),
+                                       __uint_as_float((&b4.x)[j])));
             }
           }
+          __syncwarp();
           if (g.type == kF32) {
 #pragma unroll
             for (int f = 0; f < 2; ++f)
