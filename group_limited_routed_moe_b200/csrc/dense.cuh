@@ -90,7 +90,6 @@ struct Args {
   int kblocks;     // k-blocks of a segment
   int tiles;
   int split;       // pairs that share a tile, 1 .. 4; with more than one, a cluster per tile
-  int type;        // 16-bit type of operands and outputs (Type), or kF32 outputs (kScaled)
   uint32_t idesc;
   const uint16_t* residual;        // kPlain: [M][N] or NULL
   uint8_t* saved;                  // pre-activations: kGated writes them (NULL: no), kDGate reads
@@ -374,9 +373,10 @@ __device__ __forceinline__ void load_row32(const uint16_t* p, bool row_ok, int64
 // ---------------------------------------------------------------- the pair kernel
 
 constexpr int kBM = 256;          // tile rows (128 per CTA)
-// Two epilogue warps per 32-lane quarter of tensor memory, taking its 32-column
-// chunks in turn.  (12 and 16 warps, with 128 and 96 registers a thread, made
-// the int8 product 2% faster and the gated one 3 to 10% slower at T = 8189.)
+// Two epilogue warps for each 32-lane quarter of tensor memory, taking its
+// 32-column chunks in turn.  (12 warps of 128 registers a thread made the int8
+// product 2% faster, but the gated one and its gradient 3 to 4% slower at
+// T = 8189, where the card's power bounds them; 16 warps of 96 slowed all.)
 constexpr int kEpiWarps = 8;
 constexpr int kPairThreads = 32 * (kEpiWarps + 2);
 constexpr int kABytes = 128 * kKB;
@@ -412,7 +412,7 @@ __device__ __forceinline__ void decode(const Args& g, int t, int& q, int& m, int
   m = grp * 8 + (rem - n * rows);
 }
 
-template <int KIND, bool A_MN, bool B_MN, int EPI, int BN>
+template <int KIND, bool A_MN, bool B_MN, int EPI, int BN, int TYPE>
 __global__ void __launch_bounds__(kPairThreads, 1)
     pair_gemm_kernel(const __grid_constant__ Args g) {
   using C = PairCfg<BN>;
@@ -677,7 +677,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
 #pragma unroll
           for (int i = 0; i < 16; ++i)
             pk[i] = pack2(silu(__uint_as_float(x[2 * i])) * __uint_as_float(x1[2 * i]),
-                          silu(__uint_as_float(x[2 * i + 1])) * __uint_as_float(x1[2 * i + 1]), g.type);
+                          silu(__uint_as_float(x[2 * i + 1])) * __uint_as_float(x1[2 * i + 1]), TYPE);
           store_block<2, true>(pk, stage, static_cast<uint8_t*>(P.out) + at * 2, P.N * 2, nrows, left, true, lane);
         } else if constexpr (EPI == kPlain) {
           if (g.residual != nullptr) {
@@ -685,12 +685,12 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             load_row32(g.residual + at + lane * P.N, row_ok, left, r);
 #pragma unroll
             for (int i = 0; i < 16; ++i)
-              pk[i] = pack2(__uint_as_float(x[2 * i]) + unpack_lo(r[i], g.type),
-                            __uint_as_float(x[2 * i + 1]) + unpack_hi(r[i], g.type), g.type);
+              pk[i] = pack2(__uint_as_float(x[2 * i]) + unpack_lo(r[i], TYPE),
+                            __uint_as_float(x[2 * i + 1]) + unpack_hi(r[i], TYPE), TYPE);
           } else {
 #pragma unroll
             for (int i = 0; i < 16; ++i)
-              pk[i] = pack2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]), g.type);
+              pk[i] = pack2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]), TYPE);
           }
           store_block<2, true>(pk, stage, static_cast<uint8_t*>(P.out) + at * 2, P.N * 2, nrows, left, true, lane);
         } else if constexpr (EPI == kDGate) {
@@ -705,8 +705,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
               saved_get(hw, uw, lw, j, gg, uu);
               dgate(__uint_as_float(x[2 * i + j]), gg, uu, dg[j], du[j]);
             }
-            pg[i] = pack2(dg[0], dg[1], g.type);
-            pk[i] = pack2(du[0], du[1], g.type);
+            pg[i] = pack2(dg[0], dg[1], TYPE);
+            pk[i] = pack2(du[0], du[1], TYPE);
           }
           store_block<2, true>(pg, stage, static_cast<uint8_t*>(P.out) + at * 2, P.N * 2, nrows, left, true, lane);
           store_block<2, true>(pk, stage, static_cast<uint8_t*>(g.out2) + at * 2, P.N * 2, nrows, left, true, lane);
@@ -727,7 +727,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             }
           }
           __syncwarp();
-          if (g.type == kF32) {
+          if constexpr (TYPE == kF32) {
 #pragma unroll
             for (int f = 0; f < 2; ++f)
               if (left > f * 16)
@@ -736,7 +736,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
           } else {
 #pragma unroll
             for (int i = 0; i < 16; ++i)
-              pk[i] = pack2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]), g.type);
+              pk[i] = pack2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]), TYPE);
             store_block<2, false>(pk, stage, static_cast<uint8_t*>(P.out) + at * 2, P.N * 2, nrows, left, g.vec, lane);
           }
         }

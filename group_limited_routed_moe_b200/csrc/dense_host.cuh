@@ -124,10 +124,20 @@ struct Operand {
   int64_t outer() const { return mn ? cols : rows; }
 };
 
+// The pair kernel for a tile width and a type (of the 16-bit operands and
+// outputs; of the outputs where the operands are int8).
 template <int KIND, bool A_MN, bool B_MN, int EPI>
-auto pair_kernel(int bn) -> void (*)(const dense::Args) {
-  return bn == 256 ? dense::pair_gemm_kernel<KIND, A_MN, B_MN, EPI, 256>
-                   : dense::pair_gemm_kernel<KIND, A_MN, B_MN, EPI, 128>;
+auto pair_kernel(int bn, int type) -> void (*)(const dense::Args) {
+  using namespace dense;
+  if constexpr (KIND == kI8Kind)
+    if (type == kF32)
+      return bn == 256 ? pair_gemm_kernel<KIND, A_MN, B_MN, EPI, 256, kF32>
+                       : pair_gemm_kernel<KIND, A_MN, B_MN, EPI, 128, kF32>;
+  if (type == kF16)
+    return bn == 256 ? pair_gemm_kernel<KIND, A_MN, B_MN, EPI, 256, kF16>
+                     : pair_gemm_kernel<KIND, A_MN, B_MN, EPI, 128, kF16>;
+  return bn == 256 ? pair_gemm_kernel<KIND, A_MN, B_MN, EPI, 256, kBF16>
+                   : pair_gemm_kernel<KIND, A_MN, B_MN, EPI, 128, kBF16>;
 }
 
 // What one launch computes, before a kernel is chosen for it.
@@ -145,7 +155,6 @@ struct Product {
 
 template <typename A>
 void common_args(A* g, const Product& p) {
-  g->type = p.type;
   g->residual = static_cast<const uint16_t*>(p.residual);
   g->saved = static_cast<uint8_t*>(p.saved);
   g->out2 = p.out2;
@@ -257,7 +266,7 @@ int launch_pair(const Product& p, const DeviceInfo& dev, cudaStream_t s) {
   g.idesc = dense::make_idesc(KIND, p.type, A_MN, B_MN, dense::kBM, bn);
   const int64_t clusters = g.split > 1 ? tiles : std::min<int64_t>(tiles, dev.sms / 2);
   const size_t smem = bn == 256 ? dense::PairCfg<256>::SMEM : dense::PairCfg<128>::SMEM;
-  return launch_cluster("pair_gemm_kernel launch", pair_kernel<KIND, A_MN, B_MN, EPI>(bn),
+  return launch_cluster("pair_gemm_kernel launch", pair_kernel<KIND, A_MN, B_MN, EPI>(bn, p.type),
                         static_cast<unsigned>(clusters * 2 * g.split), dense::kPairThreads, smem, 2 * g.split, s, g);
 }
 
@@ -287,6 +296,7 @@ int launch_small_rows(const Product& p, int sms, cudaStream_t s) {
   g.early = p.early;
   g.out = p.out[0];
   common_args(&g, p);
+  g.type = p.type;
   g.idesc = dense::make_idesc(KIND, p.type, W_MN, false, 128, NT);
   return launch_cluster("small_gemm_kernel launch", dense::small_gemm_kernel<KIND, W_MN, EPI, NT, ROWS>,
                         static_cast<unsigned>(tiles * g.split), dense::kSmallThreads,
@@ -323,11 +333,15 @@ int launch_product(const Product& p, const DeviceInfo& dev, cudaStream_t s) {
 
 template <int KIND, bool A_MN, bool B_MN, int EPI>
 cudaError_t pair_attr() {
-  cudaError_t e = cudaFuncSetAttribute(dense::pair_gemm_kernel<KIND, A_MN, B_MN, EPI, 256>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, dense::PairCfg<256>::SMEM);
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(dense::pair_gemm_kernel<KIND, A_MN, B_MN, EPI, 128>,
-                             cudaFuncAttributeMaxDynamicSharedMemorySize, dense::PairCfg<128>::SMEM);
+  cudaError_t e = cudaSuccess;
+  for (const int bn : {256, 128})
+    for (const int type : {dense::kBF16, dense::kF16, dense::kF32}) {
+      if (type == dense::kF32 && KIND != dense::kI8Kind) continue;
+      if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(reinterpret_cast<const void*>(pair_kernel<KIND, A_MN, B_MN, EPI>(bn, type)),
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 bn == 256 ? dense::PairCfg<256>::SMEM : dense::PairCfg<128>::SMEM);
+    }
   return e;
 }
 template <int KIND, bool W_MN, int EPI, int NT>
@@ -375,7 +389,7 @@ cudaError_t dense_setup(DeviceInfo* dev) {
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
     e = cudaOccupancyMaxActiveClusters(&dev->clusters[split],
-                                       pair_gemm_kernel<kF16Kind, false, true, kPlain, 256>, &cfg);
+                                       pair_gemm_kernel<kF16Kind, false, true, kPlain, 256, kBF16>, &cfg);
   }
   return e;
 }
