@@ -149,7 +149,6 @@ struct Product {
   const void* residual = nullptr;
   void* saved = nullptr;     // pre-activations (kGated: out, kDGate: in)
   void* out2 = nullptr;
-  bool early = false;        // follows a launch of the same call that does not write b
   const float *a_scale = nullptr, *b_scale = nullptr, *bias = nullptr;
 };
 
@@ -289,11 +288,12 @@ int launch_small_rows(const Product& p, int sms, cudaStream_t s) {
     int rc = make_map(&g.w[1], p.b[1].p, p.b[1].rows, p.b[1].cols, elem, 64);
     if (rc) return rc;
   }
-  // split k over the cluster until the CTAs fill the SMs twice, as long as
-  // each keeps 2 k-blocks
+  // split k over a cluster as long as the SMs hold all CTAs at once and each
+  // keeps 2 k-blocks (T = 16, H = 2048, I = 5632: 19.6 us; with half the CTAs
+  // 20.4, T = 1, H = 1536, I = 4096: 13.7 and 15.4)
+  const int64_t room = int64_t(sms) * dense::SmallCfg<NT, ROWS>::PER_SM;
   g.split = 1;
-  while (g.split < dense::kMaxSplit && tiles * g.split * 2 <= 2 * sms && g.kblocks * g.nseg >= g.split * 4) g.split *= 2;
-  g.early = p.early;
+  while (g.split < dense::kMaxSplit && tiles * g.split * 2 <= room && g.kblocks * g.nseg >= g.split * 4) g.split *= 2;
   g.out = p.out[0];
   common_args(&g, p);
   g.type = p.type;
@@ -543,7 +543,6 @@ int moe_gated_ffn(const void* x, const void* w_gate, const void* w_up, const voi
   down.out[0] = y;
   down.type = dtype;
   down.residual = residual;
-  down.early = true;
   return launch_product<dense::kF16Kind, true, dense::kPlain>(down, dev, s);
 }
 
@@ -602,7 +601,6 @@ int moe_gated_ffn_backward(const void* dy, const void* x, const void* w_gate, co
     p.b[0] = {w_gate, H, I, false};
     p.b[1] = {w_up, H, I, false};
     p.nseg = 2;
-    p.early = true;
     p.out[0] = dx;
     p.type = dtype;
     rc = launch_product<dense::kF16Kind, false, dense::kPlain>(p, dev, s);

@@ -27,8 +27,8 @@ constexpr int kMaxSplit = 8;
 template <int NT, int ROWS>
 struct SmallCfg {
   static constexpr int STAGE = ROWS * kKB + NT * kKB;
-  // few stages: up to 32 tokens three CTAs fit on an SM, so that the next
-  // launch's CTAs can already read weights while this one's finish
+  // 50 to 70 KB in flight; two or three CTAs fit on an SM.  With 5 stages of
+  // 128 rows, and two CTAs, T = 1 (H = 1536, I = 4096) took 14.7 us, not 13.7.
   static constexpr int STAGES = ROWS == 64 && NT <= 32 ? 5 : 3;
   // tokens of a part's row, 4 more than there are: 8 rows of 16 bytes then lie
   // in different banks
@@ -36,7 +36,13 @@ struct SmallCfg {
   static constexpr int PART = ROWS * PITCH * 4;
   static constexpr int SMEM = STAGES * STAGE + PART + 1024 + 256 + (ROWS == 64 ? 1024 : 0);
   static constexpr int TMEM = NT < 32 ? 32 : NT;
+  static constexpr int PER_SM = 232448 / (SMEM + 1024);  // CTAs an SM's shared memory holds
   static_assert((STAGES - 1) * STAGE + 128 * kKB <= SMEM - 1024, "the MMA's rows stay inside");
+  // Too large to share an SM with a kernel that takes all its tensor memory
+  // (those take 193 KB and more): a cluster whose CTAs wait for tensor memory
+  // that such a kernel holds, while that kernel waits for some they hold,
+  // cannot arise.
+  static_assert(SMEM > 40 * 1024, "shares no SM with the persistent kernels");
 };
 struct SmallTail {
   uint64_t full[8], empty[8], done, parts;
@@ -51,7 +57,6 @@ struct SmallArgs {
   int wt;                  // weight tiles
   int nseg, kblocks;       // k segments, k-blocks of a segment
   int split;               // CTAs of a cluster, 1 .. kMaxSplit
-  bool early;              // the weights may be read before the preceding launch has finished
   int type;
   uint32_t idesc;
   void* out;
@@ -126,12 +131,6 @@ __global__ void __launch_bounds__(kSmallThreads)
       tma_load_2d(sw, &g.w[seg], k0, wtile * ROWS, &S->full[s]);
     }
   };
-  // Where the launch before this one is a step of the same call (which waited
-  // for everything before it), the weights are no output of it: their first
-  // stages are read while it still runs.
-  int ahead = 0;
-  if (g.early && warp == 0 && lane == 0)
-    for (; ahead < C::STAGES && kb0 + ahead < kb1; ++ahead) load_w(kb0 + ahead, ahead);
   griddep_wait();
   griddep_launch_dependents();
 
@@ -179,7 +178,7 @@ __global__ void __launch_bounds__(kSmallThreads)
         }
         const int seg = kb >= g.kblocks ? 1 : 0;
         const int k0 = (kb - seg * g.kblocks) * KE;
-        if (it >= ahead) load_w(kb, s);
+        load_w(kb, s);
         tma_load_2d(smem_u32(smem + s * C::STAGE) + ROWS * kKB, &g.x[seg], k0, ttile * NT, &S->full[s]);
       }
       if (!ok)  // let the copies already issued land before the block can exit
