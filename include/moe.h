@@ -656,8 +656,8 @@ typedef enum moe_format { MOE_FORMAT_SAME = 0, MOE_FORMAT_INT8 = 1, MOE_FORMAT_E
  *                 whole row; the last group of a row may be shorter.
  *   scales      : fp32 [T][1] or [T][ceil(H / 128)] (out): max(amax |y| / top,
  *                 2^-126), top 127 or 448; a value is code * scale, codes are
- *                 rounded to nearest.  A NaN in a row or group makes its scale
- *                 NaN.
+ *                 rounded to nearest.  A NaN makes all its row's scales NaN; an
+ *                 infinity its own group's (its row's others have values 0).
  * 1 <= H <= 32768; rows of H % 8 == 0 take 16-byte accesses. */
 int moe_add_rmsnorm(const void* x, const void* residual, const void* weight, float eps, int64_t T,
                     int64_t H, int dtype, void* stream_out, int format, int group, void* out,
