@@ -779,59 +779,64 @@ NORM_FORMATS = {"same": 0, "int8": 1, "e4m3": 2}
 NORM_GROUP = 128
 
 
-def _expect(name: str, t: torch.Tensor, shape, dtype, device) -> None:
-    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == device \
-            and t.is_contiguous():
-        return
-    got = f"{t.dtype} {tuple(t.shape)} on {t.device}" if isinstance(t, torch.Tensor) else repr(t)
-    raise ValueError(f"{name}: expected contiguous {dtype} {tuple(shape)} on {device}, got {got}")
+def _expect(name: str, t: torch.Tensor, shape, dtype, index: int) -> None:
+    """A contiguous tensor of that shape and type on CUDA device `index`."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == index and t.is_contiguous():
+            return
+        got = f"{t.dtype} {tuple(t.shape)} on {t.device}"
+    except AttributeError:
+        got = repr(t)
+    raise ValueError(f"{name}: expected contiguous {dtype} {tuple(shape)} on cuda:{index}, got {got}")
 
 
-def _leading(name: str, t: torch.Tensor, dtypes) -> tuple[torch.device, torch.dtype]:
-    """Device and type of the tensor that sets them for a call."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dim() != 2 or t.dtype not in dtypes \
-            or not t.is_contiguous():
-        raise ValueError(f"{name}: expected a contiguous CUDA matrix of {' or '.join(map(str, dtypes))}")
-    return t.device, t.dtype
+def _leading(name: str, t: torch.Tensor, dtypes):
+    """Device index, type and sizes of the matrix that sets them for a call."""
+    if isinstance(t, torch.Tensor) and t.dtype in dtypes and t.is_contiguous():
+        index, shape = t.get_device(), t.shape
+        if index >= 0 and len(shape) == 2:
+            return index, t.dtype, shape[0], shape[1]
+    raise ValueError(f"{name}: expected a contiguous CUDA matrix of {' or '.join(map(str, dtypes))}")
 
 
 _current_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
 
 
-def _elsewhere(call, device, stream, *args, **kw):
-    """The call with `device` and, on it, `stream` made current (what the call
+def _elsewhere(call, index, stream, *args):
+    """The call with device `index` and, on it, `stream` made current (what the call
     allocates then belongs to that stream): the way of every call whose tensors
     are on another device than the current one, or that names a stream."""
-    if stream is not None and stream.device != device:
-        raise ValueError(f"stream on {stream.device}, tensors on {device}")
-    with torch.cuda.device(device), torch.cuda.stream(stream):
-        return call(*args, **kw)
+    if stream is not None and stream.device.index != index:
+        raise ValueError(f"stream on {stream.device}, tensors on cuda:{index}")
+    with torch.cuda.device(index), torch.cuda.stream(stream):
+        return call(*args)
 
 
 def _adr(t):
     return None if t is None else t.data_ptr()
 
 
-def _new(name, t, shape, dtype, device):
+# A fresh output or workspace on the current device, or the caller's, checked.
+
+def _new(name, t, shape, dtype, index):
     if t is None:
-        return torch.empty(*shape, dtype=dtype, device=device)
-    _expect(name, t, shape, dtype, device)
+        return torch.empty(*shape, dtype=dtype, device=index)
+    _expect(name, t, shape, dtype, index)
     return t
 
 
-def _new_like(name, t, like):
+def _new_like(name, t, like, index):
     if t is None:
         return torch.empty_like(like)
-    _expect(name, t, like.shape, like.dtype, like.device)
+    _expect(name, t, like.shape, like.dtype, index)
     return t
 
 
-def _scratch(name: str, t, nbytes: int, device):
-    """A workspace of at least nbytes bytes (any type), or a fresh one."""
+def _scratch(name: str, t, nbytes: int, index):
     if t is None:
-        return torch.empty(nbytes, dtype=torch.uint8, device=device)
-    if not isinstance(t, torch.Tensor) or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name}: expected contiguous memory on {device}")
+        return torch.empty(nbytes, dtype=torch.uint8, device=index)
+    if not isinstance(t, torch.Tensor) or t.get_device() != index or not t.is_contiguous():
+        raise ValueError(f"{name}: expected contiguous memory on cuda:{index}")
     return t
 
 
@@ -849,8 +854,8 @@ def moe_add_rmsnorm(x: torch.Tensor, residual: torch.Tensor | None = None, weigh
     include/moe.h).  Returns (s, out, scales): out in x's type ("same"; scales
     None), int8 or float8_e4m3fn; scales fp32 [T, 1], or [T, ceil(H / 128)]
     with group = 128.  Without residual s is x."""
-    dev, dt = _leading("x", x, _T16)
-    if stream is not None or _current_device() != dev.index:
+    dev, dt, T, H = _leading("x", x, _T16)
+    if stream is not None or _current_device() != dev:
         return _elsewhere(moe_add_rmsnorm, dev, stream, x, residual, weight, eps, out_format, group, stream_out,
                           out, scales)
     fmt = NORM_FORMATS.get(out_format)
@@ -858,7 +863,6 @@ def moe_add_rmsnorm(x: torch.Tensor, residual: torch.Tensor | None = None, weigh
         raise ValueError(f"out_format {out_format!r}: one of {sorted(NORM_FORMATS)}")
     if group and (group != NORM_GROUP or not fmt):
         raise ValueError(f"group {group}: 0, or {NORM_GROUP} with an 8-bit format")
-    T, H = x.shape
     if weight is not None:
         _expect("weight", weight, (H,), dt, dev)
     s_ptr = None
@@ -866,16 +870,16 @@ def moe_add_rmsnorm(x: torch.Tensor, residual: torch.Tensor | None = None, weigh
         stream_out = x
     else:
         _expect("residual", residual, (T, H), dt, dev)
-        stream_out = _new_like("stream_out", stream_out, x)
+        stream_out = _new_like("stream_out", stream_out, x, dev)
         s_ptr = stream_out.data_ptr()
     if fmt:
         out = _new("out", out, (T, H), torch.int8 if fmt == 1 else torch.float8_e4m3fn, dev)
         scales = _new("scales", scales, (T, -(-H // group) if group else 1), torch.float32, dev)
     else:
-        out = _new_like("out", out, x)
+        out = _new_like("out", out, x, dev)
         scales = None
     rc = lib.moe_add_rmsnorm(x.data_ptr(), _adr(residual), _adr(weight), eps, T, H, _TYPES[dt], s_ptr, fmt, group,
-                             out.data_ptr(), _adr(scales), _raw_stream(dev.index))
+                             out.data_ptr(), _adr(scales), _raw_stream(dev))
     if rc:
         _check("moe_add_rmsnorm", rc)
     return stream_out, out, scales
@@ -885,17 +889,16 @@ def moe_add_rmsnorm_backward(dy: torch.Tensor, s: torch.Tensor, weight=None, eps
                              dx=None, dweight=None, need_dweight: bool = True, workspace=None, stream=None):
     """Gradients of moe_add_rmsnorm's 16-bit form: (dx [T, H], dweight [H] fp32
     or None); dx is the gradient of x and of residual (see include/moe.h)."""
-    dev, dt = _leading("dy", dy, _T16)
-    if stream is not None or _current_device() != dev.index:
+    dev, dt, T, H = _leading("dy", dy, _T16)
+    if stream is not None or _current_device() != dev:
         return _elsewhere(moe_add_rmsnorm_backward, dev, stream, dy, s, weight, eps, dstream, dx, dweight,
                           need_dweight, workspace)
-    T, H = dy.shape
     _expect("s", s, (T, H), dt, dev)
     if weight is not None:
         _expect("weight", weight, (H,), dt, dev)
     if dstream is not None:
         _expect("dstream", dstream, (T, H), dt, dev)
-    dx = _new_like("dx", dx, dy)
+    dx = _new_like("dx", dx, dy, dev)
     if need_dweight:
         dweight = _new("dweight", dweight, (H,), torch.float32, dev)
         workspace = _scratch("workspace", workspace, lib.moe_add_rmsnorm_backward_workspace_bytes(T, H), dev)
@@ -903,7 +906,7 @@ def moe_add_rmsnorm_backward(dy: torch.Tensor, s: torch.Tensor, weight=None, eps
         dweight = workspace = None
     rc = lib.moe_add_rmsnorm_backward(dy.data_ptr(), s.data_ptr(), _adr(weight), eps, T, H, _TYPES[dt],
                                       _adr(dstream), dx.data_ptr(), _adr(dweight), _adr(workspace),
-                                      _nbytes(workspace), _raw_stream(dev.index))
+                                      _nbytes(workspace), _raw_stream(dev))
     if rc:
         _check("moe_add_rmsnorm_backward", rc)
     return dx, dweight
@@ -913,12 +916,11 @@ def moe_int8_matmul(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor, b_s
                     bias=None, out_dtype: torch.dtype = torch.bfloat16, out=None, stream=None):
     """[T, N] = (a [T, K] int8 @ b [N, K] int8 transposed) * a_scale [T] (or
     [T, 1]) * b_scale [N] + bias [N] (see include/moe.h)."""
-    dev, i8 = _leading("a", a, (torch.int8,))
-    if stream is not None or _current_device() != dev.index:
+    dev, i8, T, K = _leading("a", a, (torch.int8,))
+    if stream is not None or _current_device() != dev:
         return _elsewhere(moe_int8_matmul, dev, stream, a, a_scale, b, b_scale, bias, out_dtype, out)
     if not isinstance(b, torch.Tensor) or b.dim() != 2:
         raise ValueError("b: expected a matrix [N, K]")
-    T, K = a.shape
     N = b.shape[0]
     _expect("b", b, (N, K), i8, dev)
     _expect("a_scale", a_scale, (T, 1) if a_scale.dim() == 2 else (T,), torch.float32, dev)
@@ -929,21 +931,20 @@ def moe_int8_matmul(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor, b_s
         raise ValueError(f"out_dtype {out_dtype}: bf16, fp16 or fp32")
     out = _new("out", out, (T, N), out_dtype, dev)
     rc = lib.moe_int8_matmul(a.data_ptr(), a_scale.data_ptr(), b.data_ptr(), b_scale.data_ptr(), _adr(bias), T, N, K,
-                             _TYPES[out_dtype], out.data_ptr(), _raw_stream(dev.index))
+                             _TYPES[out_dtype], out.data_ptr(), _raw_stream(dev))
     if rc:
         _check("moe_int8_matmul", rc)
     return out
 
 
-def _ffn_shapes(x, w_gate, w_up, w_down, dev, dt):
-    T, H = x.shape
+def _ffn_weights(w_gate, w_up, w_down, H, dev, dt):
     if not isinstance(w_gate, torch.Tensor) or w_gate.dim() != 2:
         raise ValueError("w_gate: expected a matrix [H, I]")
     I = w_gate.shape[1]
     _expect("w_gate", w_gate, (H, I), dt, dev)
     _expect("w_up", w_up, (H, I), dt, dev)
     _expect("w_down", w_down, (I, H), dt, dev)
-    return T, H, I
+    return I
 
 
 def moe_gated_ffn(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, w_down: torch.Tensor,
@@ -952,17 +953,17 @@ def moe_gated_ffn(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, w_d
     x [T, H], w_gate and w_up [H, I], w_down [I, H] of one 16-bit type (see
     include/moe.h).  Returns y, or with save = True (y, saved): what
     moe_gated_ffn_backward needs of this call."""
-    dev, dt = _leading("x", x, _T16)
-    if stream is not None or _current_device() != dev.index:
+    dev, dt, T, H = _leading("x", x, _T16)
+    if stream is not None or _current_device() != dev:
         return _elsewhere(moe_gated_ffn, dev, stream, x, w_gate, w_up, w_down, residual, save, h, y)
-    T, H, I = _ffn_shapes(x, w_gate, w_up, w_down, dev, dt)
+    I = _ffn_weights(w_gate, w_up, w_down, H, dev, dt)
     if residual is not None:
         _expect("residual", residual, (T, H), dt, dev)
     h = _new("h", h, (T, I), dt, dev)
-    y = _new_like("y", y, x)
+    y = _new_like("y", y, x, dev)
     pre = torch.empty(lib.moe_gated_ffn_saved_bytes(T, I), dtype=torch.uint8, device=dev) if save else None
     rc = lib.moe_gated_ffn(x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(), w_down.data_ptr(), T, H, I, _TYPES[dt],
-                           _adr(residual), h.data_ptr(), _adr(pre), y.data_ptr(), _raw_stream(dev.index))
+                           _adr(residual), h.data_ptr(), _adr(pre), y.data_ptr(), _raw_stream(dev))
     if rc:
         _check("moe_gated_ffn", rc)
     return (y, (h, pre)) if save else y
@@ -974,21 +975,21 @@ def moe_gated_ffn_backward(dy: torch.Tensor, x: torch.Tensor, w_gate: torch.Tens
     """Gradients of moe_gated_ffn: (dx, dw_gate, dw_up, dw_down) in the inputs'
     type, None where `need` is false; `saved` from the forward call with
     save = True.  The residual's gradient is dy."""
-    dev, dt = _leading("dy", dy, _T16)
-    if stream is not None or _current_device() != dev.index:
+    dev, dt, T, H = _leading("dy", dy, _T16)
+    if stream is not None or _current_device() != dev:
         return _elsewhere(moe_gated_ffn_backward, dev, stream, dy, x, w_gate, w_up, w_down, saved, need, dx, dw_gate,
                           dw_up, dw_down, workspace)
     if len(need) != 4:
         raise ValueError("need: one truth value for each of dx, dw_gate, dw_up, dw_down")
-    T, H, I = _ffn_shapes(dy, w_gate, w_up, w_down, dev, dt)
+    I = _ffn_weights(w_gate, w_up, w_down, H, dev, dt)
     _expect("x", x, (T, H), dt, dev)
     h, pre = saved
     _expect("saved h", h, (T, I), dt, dev)
     _expect("saved pre-activations", pre, (lib.moe_gated_ffn_saved_bytes(T, I),), torch.uint8, dev)
-    dx = _new_like("dx", dx, dy) if need[0] else None
-    dw_gate = _new_like("dw_gate", dw_gate, w_gate) if need[1] else None
-    dw_up = _new_like("dw_up", dw_up, w_up) if need[2] else None
-    dw_down = _new_like("dw_down", dw_down, w_down) if need[3] else None
+    dx = _new_like("dx", dx, dy, dev) if need[0] else None
+    dw_gate = _new_like("dw_gate", dw_gate, w_gate, dev) if need[1] else None
+    dw_up = _new_like("dw_up", dw_up, w_up, dev) if need[2] else None
+    dw_down = _new_like("dw_down", dw_down, w_down, dev) if need[3] else None
     if need[0] or need[1] or need[2]:
         workspace = _scratch("workspace", workspace, lib.moe_gated_ffn_backward_workspace_bytes(T, I), dev)
     else:
@@ -996,7 +997,7 @@ def moe_gated_ffn_backward(dy: torch.Tensor, x: torch.Tensor, w_gate: torch.Tens
     rc = lib.moe_gated_ffn_backward(dy.data_ptr(), x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(),
                                     w_down.data_ptr(), h.data_ptr(), pre.data_ptr(), T, H, I, _TYPES[dt], _adr(dx),
                                     _adr(dw_gate), _adr(dw_up), _adr(dw_down), _adr(workspace), _nbytes(workspace),
-                                    _raw_stream(dev.index))
+                                    _raw_stream(dev))
     if rc:
         _check("moe_gated_ffn_backward", rc)
     return dx, dw_gate, dw_up, dw_down
@@ -1018,11 +1019,10 @@ def moe_layer_normed(x: torch.Tensor, residual, norm_weight, eps: float, packed_
                      workspace: torch.Tensor | None = None, stream=None):
     """The routed layer with its norm in front (see include/moe.h): returns
     (s, out) with s = round(x + residual), out = round(s + MoE(RMSNorm(s)))."""
-    dev, dt = _leading("x", x, (torch.bfloat16,))
-    if stream is not None or _current_device() != dev.index:
+    dev, dt, T, _ = _leading("x", x, (torch.bfloat16,))
+    if stream is not None or _current_device() != dev:
         return _elsewhere(moe_layer_normed, dev, stream, x, residual, norm_weight, eps, packed_router, bias, packed_w,
                           stream_out, out, topk_idx_out, topk_w_out, workspace)
-    T = x.shape[0]
     _expect("x", x, (T, HIDDEN), dt, dev)
     for name, t, shape, ty in (("residual", residual, (T, HIDDEN), dt), ("norm_weight", norm_weight, (HIDDEN,), dt),
                                ("bias", bias, (N_EXPERTS,), torch.float32),
@@ -1032,20 +1032,20 @@ def moe_layer_normed(x: torch.Tensor, residual, norm_weight, eps: float, packed_
             _expect(name, t, shape, ty, dev)
     for name, t, n in (("packed_router", packed_router, lib.moe_router_packed_bytes()),
                        ("packed_w", packed_w, lib.moe_packed_weight_bytes())):
-        if not isinstance(t, torch.Tensor) or t.device != dev or not t.is_contiguous() or _nbytes(t) != n:
-            raise ValueError(f"{name}: expected {n} contiguous bytes on {dev}")
+        if not isinstance(t, torch.Tensor) or t.get_device() != dev or not t.is_contiguous() or _nbytes(t) != n:
+            raise ValueError(f"{name}: expected {n} contiguous bytes on cuda:{dev}")
     s_ptr = None
     if residual is None:
         stream_out = x
     else:
-        stream_out = _new_like("stream_out", stream_out, x)
+        stream_out = _new_like("stream_out", stream_out, x, dev)
         s_ptr = stream_out.data_ptr()
-    out = _new_like("out", out, x)
+    out = _new_like("out", out, x, dev)
     if workspace is None:
         workspace = alloc_layer_normed_workspace(T, dev)
     rc = lib.moe_layer_normed(x.data_ptr(), _adr(residual), _adr(norm_weight), eps, packed_router.data_ptr(),
                               _adr(bias), packed_w.data_ptr(), T, s_ptr, out.data_ptr(), _adr(topk_idx_out),
-                              _adr(topk_w_out), workspace.data_ptr(), _nbytes(workspace), _raw_stream(dev.index))
+                              _adr(topk_w_out), workspace.data_ptr(), _nbytes(workspace), _raw_stream(dev))
     if rc:
         _check("moe_layer_normed", rc)
     return stream_out, out
