@@ -94,39 +94,40 @@ __device__ __forceinline__ float combine(float a, float b) {
   return MAX ? max_nan(a, b) : a + b;
 }
 
-// Sum (or maximum) of v over the block, in a fixed order, returned to every
-// thread.  `red` holds one word per warp; two calls in a row need different ones.
+// Sum (or maximum, of values that are not negative) of v over the block, in a
+// fixed order, returned to every thread.  `red` holds one word per warp; two
+// calls in a row need different ones.
 template <bool MAX>
 __device__ __forceinline__ float block_reduce(float v, float* red) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v = combine<MAX>(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
   if (blockDim.x == 32) return v;
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+  const int lane = threadIdx.x & 31;
+  if (lane == 0) red[threadIdx.x >> 5] = v;
   __syncthreads();
-  float r = red[0];
-  for (int w = 1; w < static_cast<int>(blockDim.x >> 5); ++w) r = combine<MAX>(r, red[w]);
-  return r;
+  v = lane < static_cast<int>(blockDim.x >> 5) ? red[lane] : 0.f;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = combine<MAX>(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+  return v;
 }
 
-// Two sums at once.
+// Two sums at once: the lower 16 lanes add up a's, the upper ones b's.
 __device__ __forceinline__ void block_sum2(float& a, float& b, float (&red)[2][32]) {
+  const int lane = threadIdx.x & 31, l = lane & 15, which = lane >> 4;
+  float v = (which ? b : a) + __shfl_xor_sync(0xFFFFFFFFu, which ? a : b, 16);
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    a += __shfl_xor_sync(0xFFFFFFFFu, a, o);
-    b += __shfl_xor_sync(0xFFFFFFFFu, b, o);
+  for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+  if (blockDim.x > 32) {
+    const int warps = blockDim.x >> 5;
+    if (l == 0) red[which][threadIdx.x >> 5] = v;
+    __syncthreads();
+    v = l < warps ? red[which][l] : 0.f;
+    if (l + 16 < warps) v += red[which][l + 16];
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
   }
-  if (blockDim.x == 32) return;
-  if ((threadIdx.x & 31) == 0) {
-    red[0][threadIdx.x >> 5] = a;
-    red[1][threadIdx.x >> 5] = b;
-  }
-  __syncthreads();
-  a = red[0][0];
-  b = red[1][0];
-  for (int w = 1; w < static_cast<int>(blockDim.x >> 5); ++w) {
-    a += red[0][w];
-    b += red[1][w];
-  }
+  a = __shfl_sync(0xFFFFFFFFu, v, 0);
+  b = __shfl_sync(0xFFFFFFFFu, v, 16);
 }
 
 __device__ __forceinline__ float scale_of(float amax, float top) {
