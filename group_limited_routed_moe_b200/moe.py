@@ -947,26 +947,43 @@ def _ffn_weights(w_gate, w_up, w_down, H, dev, dt):
     return I
 
 
+def _saved_layout(T: int, I: int) -> tuple[int, int]:
+    """Of a saved buffer: where the pre-activations begin, behind h [T, I], and
+    its bytes."""
+    at = -(-T * I * 2 // 128) * 128
+    return at, at + lib.moe_gated_ffn_saved_bytes(T, I)
+
+
 def moe_gated_ffn(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, w_down: torch.Tensor,
                   residual=None, save: bool = False, h=None, y=None, stream=None):
     """y = round(h W_down + residual), h = round(silu(x W_gate) * (x W_up)), for
     x [T, H], w_gate and w_up [H, I], w_down [I, H] of one 16-bit type (see
     include/moe.h).  Returns y, or with save = True (y, saved): what
-    moe_gated_ffn_backward needs of this call."""
+    moe_gated_ffn_backward needs of this call (h and the pre-activations, in
+    one buffer)."""
     dev, dt, T, H = _leading("x", x, _T16)
     if stream is not None or _current_device() != dev:
         return _elsewhere(moe_gated_ffn, dev, stream, x, w_gate, w_up, w_down, residual, save, h, y)
     I = _ffn_weights(w_gate, w_up, w_down, H, dev, dt)
     if residual is not None:
         _expect("residual", residual, (T, H), dt, dev)
-    h = _new("h", h, (T, I), dt, dev)
     y = _new_like("y", y, x, dev)
-    pre = torch.empty(lib.moe_gated_ffn_saved_bytes(T, I), dtype=torch.uint8, device=dev) if save else None
+    saved = pre = None
+    if save:
+        if h is not None:
+            raise ValueError("h: part of what save = True returns")
+        at, n = _saved_layout(T, I)
+        saved = torch.empty(n, dtype=torch.uint8, device=dev)
+        h_ptr = saved.data_ptr()
+        pre = h_ptr + at
+    else:
+        h = _new("h", h, (T, I), dt, dev)
+        h_ptr = h.data_ptr()
     rc = lib.moe_gated_ffn(x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(), w_down.data_ptr(), T, H, I, _TYPES[dt],
-                           _adr(residual), h.data_ptr(), _adr(pre), y.data_ptr(), _raw_stream(dev))
+                           _adr(residual), h_ptr, pre, y.data_ptr(), _raw_stream(dev))
     if rc:
         _check("moe_gated_ffn", rc)
-    return (y, (h, pre)) if save else y
+    return (y, saved) if save else y
 
 
 def moe_gated_ffn_backward(dy: torch.Tensor, x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor,
@@ -983,9 +1000,9 @@ def moe_gated_ffn_backward(dy: torch.Tensor, x: torch.Tensor, w_gate: torch.Tens
         raise ValueError("need: one truth value for each of dx, dw_gate, dw_up, dw_down")
     I = _ffn_weights(w_gate, w_up, w_down, H, dev, dt)
     _expect("x", x, (T, H), dt, dev)
-    h, pre = saved
-    _expect("saved h", h, (T, I), dt, dev)
-    _expect("saved pre-activations", pre, (lib.moe_gated_ffn_saved_bytes(T, I),), torch.uint8, dev)
+    at, n = _saved_layout(T, I)
+    _expect("saved", saved, (n,), torch.uint8, dev)
+    h_ptr = saved.data_ptr()
     dx = _new_like("dx", dx, dy, dev) if need[0] else None
     dw_gate = _new_like("dw_gate", dw_gate, w_gate, dev) if need[1] else None
     dw_up = _new_like("dw_up", dw_up, w_up, dev) if need[2] else None
@@ -995,7 +1012,7 @@ def moe_gated_ffn_backward(dy: torch.Tensor, x: torch.Tensor, w_gate: torch.Tens
     else:
         workspace = None
     rc = lib.moe_gated_ffn_backward(dy.data_ptr(), x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(),
-                                    w_down.data_ptr(), h.data_ptr(), pre.data_ptr(), T, H, I, _TYPES[dt], _adr(dx),
+                                    w_down.data_ptr(), h_ptr, h_ptr + at, T, H, I, _TYPES[dt], _adr(dx),
                                     _adr(dw_gate), _adr(dw_up), _adr(dw_down), _adr(workspace), _nbytes(workspace),
                                     _raw_stream(dev))
     if rc:

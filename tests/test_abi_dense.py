@@ -149,7 +149,7 @@ def test_binding_refuses_host_tensors():
     q, sc = torch.zeros(4, 64, dtype=torch.int8), torch.ones(4)
     for call in (lambda: moe.moe_add_rmsnorm(x), lambda: moe.moe_add_rmsnorm_backward(x, x),
                  lambda: moe.moe_int8_matmul(q, sc, q, sc), lambda: moe.moe_gated_ffn(x, w, w, w),
-                 lambda: moe.moe_gated_ffn_backward(x, x, w, w, w, (x, x)),
+                 lambda: moe.moe_gated_ffn_backward(x, x, w, w, w, x),
                  lambda: moe.moe_layer_normed(x, None, None, 1e-6, w, None, w)):
         with pytest.raises(ValueError):
             call()

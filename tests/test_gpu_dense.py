@@ -295,9 +295,11 @@ def test_ffn_refusals():
         moe.moe_gated_ffn(x, wg[:, :68].contiguous(), wu[:, :68].contiguous(), wd[:68].contiguous())
     _, saved = moe.moe_gated_ffn(x, wg, wu, wd, save=True)
     with pytest.raises(ValueError):
+        moe.moe_gated_ffn(x, wg, wu, wd, save=True, h=torch.empty(4, 72, dtype=x.dtype, device=DEV))
+    with pytest.raises(ValueError):
         moe.moe_gated_ffn_backward(dy[:3], x, wg, wu, wd, saved)
     with pytest.raises(ValueError):
-        moe.moe_gated_ffn_backward(dy, x, wg, wu, wd, (saved[0], saved[1][:16]))
+        moe.moe_gated_ffn_backward(dy, x, wg, wu, wd, saved[:-16])
     with pytest.raises(ValueError):
         moe.moe_gated_ffn_backward(dy, x, wg, wu, wd, saved, need=(True, True))
     with pytest.raises(moe.MoeError):
