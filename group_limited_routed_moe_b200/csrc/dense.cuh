@@ -84,6 +84,7 @@ struct Problem {
 constexpr int kMaxProb = 3;
 struct Args {
   CUtensorMap a[kMaxProb], b[kMaxProb];  // kGated: b[0] gate, b[1] up; segments or problems
+  CUtensorMap o[kMaxProb];               // outputs, boxes of 32 rows x 64 bytes (kDGate: dg, du)
   Problem p[kMaxProb];
   int nprob;       // products in the launch (each with a[i], b[i])
   int nseg;        // k segments of one product (a[i], b[i] summed), 1 or 2; nprob 1 then
@@ -93,9 +94,8 @@ struct Args {
   uint32_t idesc;
   const uint16_t* residual;        // kPlain: [M][N] or NULL
   uint8_t* saved;                  // pre-activations: kGated writes them (NULL: no), kDGate reads
-  void* out2;                      // kDGate: du (p[0].out is dg)
   const float *a_scale, *b_scale, *bias;  // kScaled
-  bool vec;                        // output rows are 16-byte aligned
+  bool tma_out;                    // output rows are 16-byte aligned: stored through o[]
   uint64_t timeout_ns;
 };
 
@@ -304,54 +304,68 @@ __device__ __forceinline__ void tmem_ld_32(uint32_t taddr, uint32_t (&a)[32]) {
 // ---------------------------------------------------------------- block stores
 
 constexpr int kStageRow = 64;
-constexpr int kStageWarp = 32 * kStageRow;     // one warp's block
+constexpr int kStageBlock = 32 * kStageRow;    // a warp's block of 32 rows x 64 bytes
+constexpr int kStageWarp = 2 * kStageBlock;    // two of them
 
-// Stores a warp's block of 32 rows x 64 bytes (lane = row, its 16 words in pk)
-// at g0 (row 0, first column): through the warp's shared tile (16-byte pieces of
-// a row swapped by its number, which keeps both sides free of bank conflicts),
-// so that each row leaves as one 64-byte segment.  nrows rows and `ncols` columns
-// (elements of ES bytes) of it exist.  Rows that are not 16-byte aligned go
-// out element by element, lanes along the row.
-template <int ES, bool ALWAYS_VEC>
-__device__ __forceinline__ void store_block(const uint32_t* pk, uint32_t stage, uint8_t* g0,
-                                            int64_t ld_bytes, int nrows, int64_t ncols, bool vec,
-                                            int lane) {
-  const uint32_t mine = stage + lane * kStageRow;
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, uint32_t src, int32_t c0, int32_t c1) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];\n\t"
+               "cp.async.bulk.commit_group;" ::"l"(reinterpret_cast<uint64_t>(map)),
+               "r"(src), "r"(c0), "r"(c1)
+               : "memory");
+}
+
+// A warp's block (lane = row, its 16 words in pk) into shared memory, with the
+// 64-byte swizzle of the output maps: 16-byte pieces of a row swapped by its
+// number, which keeps the writes free of bank conflicts.
+__device__ __forceinline__ void stage_block(const uint32_t* pk, uint32_t block, int lane) {
+  const uint32_t mine = block + lane * kStageRow;
 #pragma unroll
   for (int q = 0; q < 4; ++q)
     st_shared_v4(mine + ((q ^ (lane >> 1 & 3)) * 16), pk[4 * q], pk[4 * q + 1], pk[4 * q + 2], pk[4 * q + 3]);
+}
+
+// Stores a warp's block at column c0 (an element index) and row c1 by TMA,
+// which leaves out what lies outside the matrix; `turn` alternates between the
+// warp's two blocks of shared memory.  (Read back and stored by the warp's
+// lanes, a block took 600 cycles instead of 150.)
+__device__ __forceinline__ void store_block(const uint32_t* pk, uint32_t stage, int& turn, const CUtensorMap* map,
+                                            int64_t c0, int64_t c1, int lane) {
+  const uint32_t block = stage + turn * kStageBlock;
+  turn ^= 1;
+  // the store before the last one, from this block, has read it
+  if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
   __syncwarp();
-  if (ALWAYS_VEC || vec) {
-    const int row = lane >> 2, ch = lane & 3;  // and rows 8, 16, 24 further on
-    const uint32_t from = stage + row * kStageRow + ((ch ^ (row >> 1 & 3)) * 16);
-    uint8_t* to = g0 + row * ld_bytes + ch * 16;
-    const bool col_ok = (ch + 1) * (16 / ES) <= ncols;
-    uint4 v[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = ld_shared_v4(from + i * 8 * kStageRow);
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (col_ok && row + i * 8 < nrows) st_global_v4(to + i * 8 * ld_bytes, v[i].x, v[i].y, v[i].z, v[i].w);
-  } else {
-    constexpr int PER = 64 / ES;               // elements of a row: 32 or 16
-    const int col = lane % PER;
-    for (int r = lane / PER; r < nrows; r += 32 / PER) {
-      if (col < ncols) {
-        if constexpr (ES == 2) {
-          uint16_t v;
-          asm volatile("ld.shared.b16 %0, [%1];"
-                       : "=h"(v)
-                       : "r"(stage + r * kStageRow + ((col / 8 ^ (r >> 1 & 3)) * 16) + col % 8 * 2)
-                       : "memory");
-          *reinterpret_cast<uint16_t*>(g0 + r * ld_bytes + col * 2) = v;
-        } else {
-          uint32_t v;
-          asm volatile("ld.shared.b32 %0, [%1];"
-                       : "=r"(v)
-                       : "r"(stage + r * kStageRow + ((col / 4 ^ (r >> 1 & 3)) * 16) + col % 4 * 4)
-                       : "memory");
-          *reinterpret_cast<uint32_t*>(g0 + r * ld_bytes + col * 4) = v;
-        }
+  stage_block(pk, block, lane);
+  fence_proxy_async_smem();
+  __syncwarp();
+  if (lane == 0) tma_store_2d(map, block, static_cast<int32_t>(c0), static_cast<int32_t>(c1));
+}
+
+// The same for rows that are not 16-byte aligned, element by element (of ES
+// bytes), lanes along the row; nrows rows and ncols columns of the block exist.
+template <int ES>
+__device__ __forceinline__ void store_block_ragged(const uint32_t* pk, uint32_t block, uint8_t* g0, int64_t ld_bytes,
+                                                   int nrows, int64_t ncols, int lane) {
+  stage_block(pk, block, lane);
+  __syncwarp();
+  constexpr int PER = 64 / ES;  // elements of a row: 32 or 16
+  const int col = lane % PER;
+  for (int r = lane / PER; r < nrows; r += 32 / PER) {
+    if (col < ncols) {
+      if constexpr (ES == 2) {
+        uint16_t v;
+        asm volatile("ld.shared.b16 %0, [%1];"
+                     : "=h"(v)
+                     : "r"(block + r * kStageRow + ((col / 8 ^ (r >> 1 & 3)) * 16) + col % 8 * 2)
+                     : "memory");
+        *reinterpret_cast<uint16_t*>(g0 + r * ld_bytes + col * 2) = v;
+      } else {
+        uint32_t v;
+        asm volatile("ld.shared.b32 %0, [%1];"
+                     : "=r"(v)
+                     : "r"(block + r * kStageRow + ((col / 4 ^ (r >> 1 & 3)) * 16) + col % 4 * 4)
+                     : "memory");
+        *reinterpret_cast<uint32_t*>(g0 + r * ld_bytes + col * 4) = v;
       }
     }
   }
@@ -448,6 +462,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   }
   if (warp == kTmaWarp && lane == 0) {
     for (int i = 0; i < kMaxProb; ++i) {
+      if (g.tma_out && i < g.nprob + (EPI == kDGate)) tma_prefetch_desc(&g.o[i]);
       if (i < max(g.nprob, g.nseg)) tma_prefetch_desc(&g.a[i]);
       if (i < max(g.nprob, g.nseg) + (EPI == kGated)) tma_prefetch_desc(&g.b[i]);
     }
@@ -551,7 +566,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     // ---------------------------------------------- epilogue
     const int quarter = warp & 3, sub = warp >> 2;
     const uint32_t stage = smem_u32(sEpi + warp * kStageWarp);
-    int n_tile = 0;
+    int n_tile = 0, turn = 0;
     for (int t = cluster; t < g.tiles; t += nclusters, ++n_tile) {
       int q, m, n;
       decode(g, t, q, m, n);
@@ -678,7 +693,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
           for (int i = 0; i < 16; ++i)
             pk[i] = pack2(silu(__uint_as_float(x[2 * i])) * __uint_as_float(x1[2 * i]),
                           silu(__uint_as_float(x[2 * i + 1])) * __uint_as_float(x1[2 * i + 1]), TYPE);
-          store_block<2, true>(pk, stage, static_cast<uint8_t*>(P.out) + at * 2, P.N * 2, nrows, left, true, lane);
+          store_block(pk, stage, turn, &g.o[0], col, row0, lane);
         } else if constexpr (EPI == kPlain) {
           if (g.residual != nullptr) {
             uint32_t r[16];
@@ -692,7 +707,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             for (int i = 0; i < 16; ++i)
               pk[i] = pack2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]), TYPE);
           }
-          store_block<2, true>(pk, stage, static_cast<uint8_t*>(P.out) + at * 2, P.N * 2, nrows, left, true, lane);
+          store_block(pk, stage, turn, &g.o[q], col, row0, lane);
         } else if constexpr (EPI == kDGate) {
           uint32_t pg[16];
 #pragma unroll
@@ -708,17 +723,20 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             pg[i] = pack2(dg[0], dg[1], TYPE);
             pk[i] = pack2(du[0], du[1], TYPE);
           }
-          store_block<2, true>(pg, stage, static_cast<uint8_t*>(P.out) + at * 2, P.N * 2, nrows, left, true, lane);
-          store_block<2, true>(pk, stage, static_cast<uint8_t*>(g.out2) + at * 2, P.N * 2, nrows, left, true, lane);
+          store_block(pg, stage, turn, &g.o[0], col, row0, lane);
+          store_block(pk, stage, turn, &g.o[1], col, row0, lane);
         } else {
-          // the 32 columns' values to every lane, through the warp's shared tile
-          asm volatile("st.shared.f32 [%0], %1;" ::"r"(stage + lane * 4), "f"(sb) : "memory");
-          asm volatile("st.shared.f32 [%0], %1;" ::"r"(stage + 128 + lane * 4), "f"(bi) : "memory");
+          // the 32 columns' values to every lane, through the block that is stored next
+          const uint32_t scales = stage + turn * kStageBlock;
+          if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+          __syncwarp();
+          asm volatile("st.shared.f32 [%0], %1;" ::"r"(scales + lane * 4), "f"(sb) : "memory");
+          asm volatile("st.shared.f32 [%0], %1;" ::"r"(scales + 128 + lane * 4), "f"(bi) : "memory");
           __syncwarp();
           column_scales(ch + kEpiWarps / 4);
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            const uint4 s4 = ld_shared_v4(stage + i * 16), b4 = ld_shared_v4(stage + 128 + i * 16);
+            const uint4 s4 = ld_shared_v4(scales + i * 16), b4 = ld_shared_v4(scales + 128 + i * 16);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
               uint32_t& v = x[4 * i + j];
@@ -727,21 +745,27 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             }
           }
           __syncwarp();
-          if constexpr (TYPE == kF32) {
-#pragma unroll
-            for (int f = 0; f < 2; ++f)
-              if (left > f * 16)
-                store_block<4, false>(x + f * 16, stage, static_cast<uint8_t*>(P.out) + (at + f * 16) * 4, P.N * 4,
-                                      nrows, left - f * 16, g.vec, lane);
-          } else {
+          constexpr int ES = TYPE == kF32 ? 4 : 2, NB = TYPE == kF32 ? 2 : 1, PER = 64 / ES;  // blocks, their columns
+          if constexpr (TYPE != kF32) {
 #pragma unroll
             for (int i = 0; i < 16; ++i)
-              pk[i] = pack2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]), TYPE);
-            store_block<2, false>(pk, stage, static_cast<uint8_t*>(P.out) + at * 2, P.N * 2, nrows, left, g.vec, lane);
+              x[i] = pack2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]), TYPE);
+          }
+#pragma unroll
+          for (int f = 0; f < NB; ++f) {
+            if (left <= f * PER) break;
+            if (g.tma_out)
+              store_block(x + f * 16, stage, turn, &g.o[0], col + f * PER, row0, lane);
+            else
+              store_block_ragged<ES>(x + f * 16, stage, static_cast<uint8_t*>(P.out) + (at + f * PER) * ES, P.N * ES,
+                                     nrows, left - f * PER, lane);
           }
         }
       }
     }
+    // the stores have been made before the block exits
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    __syncwarp();
   }
   if (g.split > 1 && warp >= kEpiWarps) {  // the epilogue warps' barrier after the products
     __syncwarp();

@@ -99,16 +99,22 @@ constexpr int64_t kMaxDim = 65536;        // widths of the gated block
 constexpr int64_t kMaxInt8N = 1 << 20;    // channels of the int8 product
 constexpr int64_t kMaxInt8K = 131056;     // K * 128 * 128 < 2^31: the int32 sums cannot overflow
 
-// Row-major matrix of `rows` rows of `cols` elements (1 or 2 bytes), boxes of
-// 128 bytes x box_rows, 128-byte swizzle; outside the matrix reads zero.
-int make_map(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int elem, int box_rows) {
+// Row-major matrix of `rows` rows of `cols` elements (of 1, 2 or 4 bytes), boxes
+// of box_bytes x box_rows with the swizzle of that width: 128 bytes for the
+// operands (outside the matrix reads zero), 64 for the outputs.
+int make_map(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int elem, int box_rows,
+             int box_bytes = 128) {
   const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
   const cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols) * elem};
-  const cuuint32_t box[2] = {static_cast<cuuint32_t>(128 / elem), static_cast<cuuint32_t>(box_rows)};
+  const cuuint32_t box[2] = {static_cast<cuuint32_t>(box_bytes / elem), static_cast<cuuint32_t>(box_rows)};
   const cuuint32_t estr[2] = {1, 1};
-  const CUresult r = g_encode(m, elem == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 2,
-                              const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+  const CUtensorMapDataType type = elem == 1   ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                                   : elem == 2 ? CU_TENSOR_MAP_DATA_TYPE_UINT16
+                                               : CU_TENSOR_MAP_DATA_TYPE_UINT32;
+  const CUresult r = g_encode(m, type, 2, const_cast<void*>(base), dims, strides, box, estr,
+                              CU_TENSOR_MAP_INTERLEAVE_NONE,
+                              box_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return fail(MOE_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", int(r));
   return MOE_OK;
@@ -156,7 +162,6 @@ template <typename A>
 void common_args(A* g, const Product& p) {
   g->residual = static_cast<const uint16_t*>(p.residual);
   g->saved = static_cast<uint8_t*>(p.saved);
-  g->out2 = p.out2;
   g->a_scale = p.a_scale;
   g->b_scale = p.b_scale;
   g->bias = p.bias;
@@ -237,7 +242,9 @@ int launch_pair(const Product& p, const DeviceInfo& dev, cudaStream_t s) {
   const int bn = shape.bn;
   g.split = shape.split;
   int64_t tiles = 0;
-  g.vec = true;
+  const int out_elem = p.type == dense::kF32 ? 4 : 2;
+  g.tma_out = true;  // unless some product's rows are not whole 16-byte pieces
+  for (int i = 0; i < p.nprob; ++i) g.tma_out = g.tma_out && p.b[i].outer() * out_elem % 16 == 0;
   g.nprob = 0;
   for (int i = 0; i < std::max(p.nprob, p.nseg); ++i) {  // products, or segments of one
     if (p.nprob > 1 && p.out[i] == nullptr) continue;
@@ -254,7 +261,9 @@ int launch_pair(const Product& p, const DeviceInfo& dev, cudaStream_t s) {
     q.tile0 = static_cast<int>(tiles);
     q.out = p.out[i];
     tiles += int64_t(q.mt) * q.nt;
-    g.vec = g.vec && (q.N * (p.type == dense::kF32 ? 4 : 2)) % 16 == 0;
+    if (g.tma_out) rc = make_map(&g.o[j], q.out, q.M, q.N, out_elem, 32, 64);
+    if (!rc && EPI == dense::kDGate) rc = make_map(&g.o[1], p.out2, q.M, q.N, out_elem, 32, 64);
+    if (rc) return rc;
   }
   if (EPI == dense::kGated) {  // b[1]: the up weights
     int rc = make_map(&g.b[1], p.b[1].p, p.b[1].rows, p.b[1].cols, elem, 64);
@@ -296,6 +305,7 @@ int launch_small_rows(const Product& p, int sms, cudaStream_t s) {
   while (g.split < dense::kMaxSplit && tiles * g.split * 2 <= room && g.kblocks * g.nseg >= g.split * 4) g.split *= 2;
   g.out = p.out[0];
   common_args(&g, p);
+  g.out2 = p.out2;
   g.type = p.type;
   g.idesc = dense::make_idesc(KIND, p.type, W_MN, false, 128, NT);
   return launch_cluster("small_gemm_kernel launch", dense::small_gemm_kernel<KIND, W_MN, EPI, NT, ROWS>,
