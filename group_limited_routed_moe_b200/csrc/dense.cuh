@@ -327,7 +327,7 @@ __device__ __forceinline__ void stage_block(const uint32_t* pk, uint32_t block, 
 // Stores a warp's block at column c0 (an element index) and row c1 by TMA,
 // which leaves out what lies outside the matrix; `turn` alternates between the
 // warp's two blocks of shared memory.  (Read back and stored by the warp's
-// lanes, a block took 600 cycles instead of 150.)
+// lanes, a block took 600 cycles instead of 420.)
 __device__ __forceinline__ void store_block(const uint32_t* pk, uint32_t stage, int& turn, const CUtensorMap* map,
                                             int64_t c0, int64_t c1, int lane) {
   const uint32_t block = stage + turn * kStageBlock;
