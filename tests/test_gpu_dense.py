@@ -393,3 +393,75 @@ def test_training_step_of_a_dense_layer(T, dtype):
     for name, a, v in zip(("y", "dx", "dw", "dwg", "dwu", "dwd"), (y, dx, dw, dwg, dwu, dwd), (Y.detach(), *want)):
         err = float((a.cpu().double() - v).norm() / v.norm())
         assert err <= 12 * _u(dt), f"{name}: {err:.3g}"
+
+
+@pytest.mark.parametrize("T", [1, 37, 300])
+def test_back_to_back(T):
+    """A run of different calls without a wait between them (each may start
+    while the one before finishes) gives what it gives with a wait after each."""
+    from gpu_helpers import layer0_weights
+    H, I = 1536, 1032
+    x, wg, wu, wd, r, dy = (t.to(DEV) for t in _ffn_inputs(T, H, I, torch.bfloat16, T))
+    g = torch.Generator().manual_seed(T)
+    router = moe.moe_pack_router((0.05 * torch.randn(H, 128, generator=g)).bfloat16().to(DEV))
+    b = torch.randint(-127, 128, (H, H), generator=g, dtype=torch.int8).to(DEV)
+    sb = torch.full((H,), 1e-4, device=DEV)
+    packed = layer0_weights().packed
+
+    def run(wait):
+        outs, s = [], x
+        for _ in range(3):
+            s, n, _ = moe.moe_add_rmsnorm(s, r)
+            wait()
+            y, saved = moe.moe_gated_ffn(n, wg, wu, wd, residual=s, save=True)
+            wait()
+            grads = moe.moe_gated_ffn_backward(dy, n, wg, wu, wd, saved)
+            wait()
+            dx, dw = moe.moe_add_rmsnorm_backward(grads[0], s, dstream=dy)
+            wait()
+            _, q, sc = moe.moe_add_rmsnorm(y, r, out_format="int8")
+            wait()
+            z = moe.moe_int8_matmul(q, sc, b, sb)
+            wait()
+            s, out = moe.moe_layer_normed(z, y, None, 1e-6, router, None, packed)
+            wait()
+            outs += [y, *grads, dx, dw, z, s, out]
+            s = out
+        return outs
+    want = run(torch.cuda.synchronize)
+    torch.cuda.synchronize()
+    for _ in range(5):
+        got = run(lambda: None)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, c) for a, c in zip(want, got))
+    assert moe.get_device_status(0) == moe.MOE_OK
+
+
+def test_beside_the_routed_layer():
+    """Dense products on one stream while routed layers run on another: neither
+    waits for the other for good, and both give what they give alone."""
+    from gpu_helpers import layer0_weights
+    from group_limited_routed_moe_b200 import synth
+    packed = layer0_weights().packed
+    jobs = []
+    for T in (2, 300):
+        tok = synth.make_tokens(T, seed=1)
+        lx = torch.from_numpy(tok.x_bits.view("int16")).to(DEV).view(torch.bfloat16)
+        lg, bias = torch.from_numpy(tok.logits).to(DEV), torch.from_numpy(tok.bias).to(DEV)
+        jobs.append(lambda lx=lx, lg=lg, bias=bias: moe.moe_layer(lx, lg, bias, packed))
+    dense = []
+    for T in (1, 50, 400):
+        x, wg, wu, wd, r, dy = (t.to(DEV) for t in _ffn_inputs(T, 512, 1032, torch.bfloat16, T))
+        dense.append(lambda x=x, wg=wg, wu=wu, wd=wd, r=r: moe.moe_gated_ffn(x, wg, wu, wd, residual=r))
+    want = [[f() for f in jobs], [f() for f in dense]]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [[], []]
+    for _ in range(20):
+        for i, fs in enumerate((jobs, dense)):
+            with torch.cuda.stream(streams[i]):
+                got[i].append([f() for f in fs])
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(a, c) for run in got[i] for a, c in zip(want[i], run))
+    assert moe.get_device_status(0) == moe.MOE_OK
