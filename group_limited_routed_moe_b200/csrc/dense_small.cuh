@@ -136,7 +136,8 @@ __global__ void __launch_bounds__(kSmallThreads)
 
   // The outputs this CTA owns: unit e is column e % own of its share and the 4
   // tokens from e / own * 4 on.  What the epilogue reads of a thread's next
-  // unit is loaded ahead, the first one's before the products.
+  // unit is loaded ahead, the first one's during the products (after their own
+  // part by the two warps that drive them: they would start later).
   constexpr int PER = EPI == kGated ? 64 : ROWS;
   const int own = PER / g.split;                // output columns a rank owns
   const int rows = ROWS / g.split;              // rows of a part
@@ -164,7 +165,7 @@ __global__ void __launch_bounds__(kSmallThreads)
       }
     }
   };
-  fetch(threadIdx.x);
+  if (warp >= 2) fetch(threadIdx.x);
 
   if (warp == 0) {
     if (lane == 0) {
@@ -203,6 +204,7 @@ __global__ void __launch_bounds__(kSmallThreads)
     }
   }
   __syncwarp();
+  if (warp < 2) fetch(threadIdx.x);
   bool ok = mbar_wait(&S->done, 0, abort_flag, 2 * g.timeout_ns, kSiteSmallDone);
   ok = __syncthreads_and(ok && !*abort_flag) != 0;
   tc_fence_after();
