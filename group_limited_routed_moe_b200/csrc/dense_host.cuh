@@ -202,7 +202,7 @@ struct PairShape {
 
 // The choice with the smallest estimate.  Measured at T = 96 .. 2048 tokens and
 // widths of 512 to 4096: a k-block takes a pair 300 ns (256 columns) or 290 ns
-// (128; both wait for L2), everything else 7.2 or 5.6 us, and sharing a tile
+// (128; both wait for L2), everything else 6.5 or 5.0 us, and sharing a tile
 // 2.2 us more, or 0.9 us and 0.6 us for each pair above two.  E.g. T = 256,
 // N = K = 4096 in int8: 16 tiles of 256 columns 16.8 us, shared by two pairs
 // 14.2, by four 24 (two rounds of clusters); 32 tiles of 128 columns 15.0,
@@ -219,7 +219,7 @@ PairShape pair_shape(const Product& p, int64_t kbs, const DeviceInfo& dev) {
       if (split > 1 && (tiles > dev.clusters[split] || kbs < 4 * split)) continue;
       const int64_t rounds = split > 1 ? 1 : div_up(tiles, dev.sms / 2);
       const int64_t share = split == 1 ? 0 : bn == 256 ? 2200 : 900 + 600 * (split - 2);
-      const int64_t ns = rounds * div_up(kbs, split) * (bn == 256 ? 300 : 290) + (bn == 256 ? 7200 : 5600) + share;
+      const int64_t ns = rounds * div_up(kbs, split) * (bn == 256 ? 300 : 290) + (bn == 256 ? 6500 : 5000) + share;
       if (ns < best.ns) best = {bn, split, ns};
     }
   }
@@ -278,6 +278,16 @@ int launch_pair(const Product& p, const DeviceInfo& dev, cudaStream_t s) {
                         static_cast<unsigned>(clusters * 2 * g.split), dense::kPairThreads, smem, 2 * g.split, s, g);
 }
 
+// CTAs that share a few-token tile's k range: a power of two, as long as the
+// SMs have room for all CTAs at once and each keeps 2 k-blocks (T = 16,
+// H = 2048, I = 5632: 19.6 us; with half the CTAs 20.4, T = 1, H = 1536,
+// I = 4096: 13.7 and 15.4).
+int small_split(int64_t tiles, int64_t kbs, int64_t room) {
+  int split = 1;
+  while (split < dense::kMaxSplit && tiles * split * 2 <= room && kbs >= split * 4) split *= 2;
+  return split;
+}
+
 template <int KIND, bool W_MN, int EPI, int NT, int ROWS>
 int launch_small_rows(const Product& p, int sms, cudaStream_t s) {
   const int elem = KIND == dense::kI8Kind ? 1 : 2, ke = 128 / elem;
@@ -297,12 +307,7 @@ int launch_small_rows(const Product& p, int sms, cudaStream_t s) {
     int rc = make_map(&g.w[1], p.b[1].p, p.b[1].rows, p.b[1].cols, elem, 64);
     if (rc) return rc;
   }
-  // split k over a cluster as long as the SMs hold all CTAs at once and each
-  // keeps 2 k-blocks (T = 16, H = 2048, I = 5632: 19.6 us; with half the CTAs
-  // 20.4, T = 1, H = 1536, I = 4096: 13.7 and 15.4)
-  const int64_t room = int64_t(sms) * dense::SmallCfg<NT, ROWS>::PER_SM;
-  g.split = 1;
-  while (g.split < dense::kMaxSplit && tiles * g.split * 2 <= room && g.kblocks * g.nseg >= g.split * 4) g.split *= 2;
+  g.split = small_split(tiles, int64_t(g.kblocks) * g.nseg, int64_t(sms) * dense::SmallCfg<NT, ROWS>::PER_SM);
   g.out = p.out[0];
   common_args(&g, p);
   g.out2 = p.out2;
@@ -316,19 +321,25 @@ int launch_small_rows(const Product& p, int sms, cudaStream_t s) {
 template <int KIND, bool W_MN, int EPI, int NT>
 int launch_small_nt(const Product& p, int sms, cudaStream_t s) {
   if constexpr (EPI != dense::kGated) {
-    // tiles of 64 weight rows where 128-row tiles, split as far as they go,
-    // are fewer than the SMs
-    const int64_t tiles = div_up(p.b[0].outer(), 128) * div_up(p.a[0].outer(), NT);
-    if (tiles * dense::kMaxSplit < sms) return launch_small_rows<KIND, W_MN, EPI, NT, 64>(p, sms, s);
+    // Tiles of 64 weight rows where 128-row tiles, split as far as they go, are
+    // fewer than the SMs; with more than two token tiles already where they
+    // would have to share SMs for it (H = 1536, I = 4096, dh and dx: T = 192
+    // 28.8 us against 33.1 with 128 rows, but T = 128 26.1 against 23.8).
+    const int64_t token_tiles = div_up(p.a[0].outer(), NT);
+    const int64_t tiles = div_up(p.b[0].outer(), 128) * token_tiles;
+    const int64_t room = token_tiles > 2 ? sms : int64_t(sms) * dense::SmallCfg<NT, 128>::PER_SM;
+    if (tiles * small_split(tiles, all_kblocks<KIND>(p), room) < sms)
+      return launch_small_rows<KIND, W_MN, EPI, NT, 64>(p, sms, s);
   }
   return launch_small_rows<KIND, W_MN, EPI, NT, 128>(p, sms, s);
 }
 
 // One product of T tokens with weights.  Up to 32 tokens the weights are the
-// MMA's rows; above, by the estimate of both ways: with the weights as rows
-// 4.5 us and 0.5 us for each k-block (128 weight rows x 64 tokens) that an SM
-// gets, measured over the sizes that pair_shape names (T = 256, K = 1536,
-// int8: N = 512 4.7 us against 8.0 on pairs, N = 4096 10.9 against 8.7).
+// MMA's rows; above, by the estimate of both ways: with the weights as rows 4 us,
+// 0.38 us for each k-block (128 weight rows x 64 tokens) and 2 us for each tile
+// that an SM gets, measured over the sizes that pair_shape names (int8, N = 4096:
+// T = 128, K = 4096 9.4 us against 11.3 on pairs, T = 256 13.0 against 11.4,
+// T = 192, K = 1536 9.4 against 8.3; N = 512, T = 256, K = 1536 4.2 against 7.7).
 template <int KIND, bool B_MN, int EPI>
 int launch_product(const Product& p, const DeviceInfo& dev, cudaStream_t s) {
   const int64_t T = p.a[0].outer();
@@ -336,7 +347,7 @@ int launch_product(const Product& p, const DeviceInfo& dev, cudaStream_t s) {
   if (T <= 32) return launch_small_nt<KIND, B_MN, EPI, 32>(p, dev.sms, s);
   const int64_t tiles = div_up(p.b[0].outer(), EPI == dense::kGated ? 64 : 128) * div_up(T, 64);
   const int64_t kbs = all_kblocks<KIND>(p);
-  if (4500 + tiles * kbs * 500 / dev.sms <= pair_shape<EPI>(p, kbs, dev).ns)
+  if (4000 + tiles * (kbs * 380 + 2000) / dev.sms <= pair_shape<EPI>(p, kbs, dev).ns)
     return launch_small_nt<KIND, B_MN, EPI, 64>(p, dev.sms, s);
   return launch_pair<KIND, false, B_MN, EPI>(p, dev, s);
 }
