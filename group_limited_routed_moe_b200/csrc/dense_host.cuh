@@ -71,11 +71,12 @@ int launch_norm_bwd(int64_t T, const void* dy, const void* sv, const void* w, fl
                     const void* dstream, void* dx, float* parts, int blocks, cudaStream_t s) {
   const RowShape rs = row_shape(H / VEC);
   return with_row_shape<VEC>(rs, [&](auto nv, auto maxt) {
-    return launch_pdl("rmsnorm_backward_kernel launch",
-                      norm::rmsnorm_backward_kernel<E, VEC, decltype(nv)::value, decltype(maxt)::value>,
-                      dim3(blocks), dim3(rs.threads), 0, s, static_cast<const E*>(dy), static_cast<const E*>(sv),
-                      static_cast<const E*>(w), eps, T, H, static_cast<const E*>(dstream), static_cast<E*>(dx),
-                      parts);
+    constexpr int NV = decltype(nv)::value, MAXT = decltype(maxt)::value;
+    auto k = eps > 0.f ? norm::rmsnorm_backward_kernel<E, VEC, NV, MAXT, false>
+                       : norm::rmsnorm_backward_kernel<E, VEC, NV, MAXT, true>;
+    return launch_pdl("rmsnorm_backward_kernel launch", k, dim3(blocks), dim3(rs.threads), 0, s,
+                      static_cast<const E*>(dy), static_cast<const E*>(sv), static_cast<const E*>(w), eps, T, H,
+                      static_cast<const E*>(dstream), static_cast<E*>(dx), parts);
   });
 }
 

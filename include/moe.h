@@ -644,7 +644,9 @@ typedef enum moe_format { MOE_FORMAT_SAME = 0, MOE_FORMAT_INT8 = 1, MOE_FORMAT_E
 /* Residual addition and root-mean-square norm:
  *   s[t] = round(x[t] + residual[t])  (one rounding; x itself without residual)
  *   y[t][c] = s[t][c] * weight[c] / sqrt(mean_c s[t][c]^2 + eps)
- * in fp32 (rows whose sum of squares leaves its range are scaled first).
+ * in fp32 (rows whose sum of squares leaves its range, underflowing to zero
+ * included, are scaled first).  0 <= eps; a row of zeros gives zeros, with
+ * eps = 0 the formula's 0 / 0: NaN, in that row alone.
  *   x, residual : [T][H] of `dtype` (bf16 or fp16); residual may be NULL
  *   weight      : [H] of `dtype`, or NULL for ones
  *   stream_out  : [T][H] (out), s; required with residual, not written without.
@@ -672,7 +674,8 @@ size_t moe_add_rmsnorm_backward_workspace_bytes(int64_t T, int64_t H);
  *   dx      : [T][H] (out) gradient of s, which is that of x and of residual
  *   dweight : fp32 [H] (out), or NULL.  Summed in a fixed order.
  * dy, s, weight, dstream and dx are of `dtype`; dx must alias no input.
- * T == 0 sets dweight to zero. */
+ * T == 0 sets dweight to zero.  With eps = 0 a row of zeros has no gradient: its
+ * dx is NaN, and so is dweight. */
 int moe_add_rmsnorm_backward(const void* dy, const void* s, const void* weight, float eps, int64_t T,
                              int64_t H, int dtype, const void* dstream, void* dx, float* dweight,
                              void* workspace, size_t workspace_bytes, moe_stream_t stream);
