@@ -134,15 +134,27 @@ __device__ __forceinline__ float scale_of(float amax, float top) {
   return max_nan(__fdiv_rn(amax, top), 1.17549435e-38f);
 }
 
+// The codes of values that share a scale: round(y / scale).  The quotient is
+// that by the reciprocal, corrected once by its exact remainder, which makes it
+// the correctly rounded one (Markstein 1990).  Without it values beside a tie
+// (half a group's largest, for one) took the other code.  int8 at T = 8189,
+// H = 4096: 43.9 us, 42.0 without the correction, 49.1 with a division for each
+// value.
 template <int FMT>
-__device__ __forceinline__ uint8_t code_of(float y, float inv) {
-  if constexpr (FMT == kInt8) {
-    const int q = __float2int_rn(y * inv);
-    return static_cast<uint8_t>(max(-127, min(127, q)));
-  } else {
-    return __nv_cvt_float_to_fp8(y * inv, __NV_SATFINITE, __NV_E4M3);
+struct Coder {
+  float scale, inv;  // an infinite scale, whose reciprocal is 0, is kept as 0: finite values give 0
+  __device__ __forceinline__ explicit Coder(float s) : scale(s == INFINITY ? 0.f : s), inv(1.f / s) {}
+  __device__ __forceinline__ uint8_t operator()(float y) const {
+    float z = y * inv;
+    z = fmaf(fmaf(-z, scale, y), inv, z);
+    if constexpr (FMT == kInt8) {
+      const int q = __float2int_rn(z);
+      return static_cast<uint8_t>(max(-127, min(127, q)));
+    } else {
+      return __nv_cvt_float_to_fp8(z, __NV_SATFINITE, __NV_E4M3);
+    }
   }
-}
+};
 
 template <typename E, int VEC>
 __device__ __forceinline__ void load_weight(const E* w, int p, float (&f)[VEC]) {
@@ -300,10 +312,10 @@ __global__ void __launch_bounds__(MAXT)
         if (p < nvec && (p * VEC) % kGroup == 0) scales[row * ngroups + p * VEC / kGroup] = scale;
       }
       if (p < nvec) {
-        const float inv = 1.f / scale;
+        const Coder<FMT> code(scale);
         Codes<VEC> o;
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) o.e[j] = code_of<FMT>(v[i][j], inv);
+        for (int j = 0; j < VEC; ++j) o.e[j] = code(v[i][j]);
         *reinterpret_cast<Codes<VEC>*>(static_cast<uint8_t*>(out) + base +
                                                static_cast<int64_t>(p) * VEC) = o;
       }
