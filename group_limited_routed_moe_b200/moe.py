@@ -1060,6 +1060,8 @@ def moe_layer_normed(x: torch.Tensor, residual, norm_weight, eps: float, packed_
     out = _new_like("out", out, x, dev)
     if workspace is None:
         workspace = alloc_layer_normed_workspace(T, dev)
+    else:
+        _scratch("workspace", workspace, 0, dev)
     rc = lib.moe_layer_normed(x.data_ptr(), _adr(residual), _adr(norm_weight), eps, packed_router.data_ptr(),
                               _adr(bias), packed_w.data_ptr(), T, s_ptr, out.data_ptr(), _adr(topk_idx_out),
                               _adr(topk_w_out), workspace.data_ptr(), _nbytes(workspace), _raw_stream(dev))
