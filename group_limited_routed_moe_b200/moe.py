@@ -923,7 +923,7 @@ def moe_int8_matmul(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor, b_s
         raise ValueError("b: expected a matrix [N, K]")
     N = b.shape[0]
     _expect("b", b, (N, K), i8, dev)
-    _expect("a_scale", a_scale, (T, 1) if a_scale.dim() == 2 else (T,), torch.float32, dev)
+    _expect("a_scale", a_scale, (T, 1) if getattr(a_scale, "ndim", 1) == 2 else (T,), torch.float32, dev)
     _expect("b_scale", b_scale, (N,), torch.float32, dev)
     if bias is not None:
         _expect("bias", bias, (N,), torch.float32, dev)

@@ -77,3 +77,12 @@ def test_backward_workspaces(no_library, which):
     with pytest.raises(ValueError, match="workspace"):
         moe.moe_gated_ffn_backward(x, x, w, w, wd, saved, dx=dev((T, H)), dw_gate=dev((H, I)), dw_up=dev((H, I)),
                                    dw_down=dev((I, H)), workspace=ws)
+
+
+@pytest.mark.parametrize("name", ["a", "a_scale", "b", "b_scale", "bias", "out"])
+def test_int8_arguments_that_are_no_tensors(no_library, name):
+    args = {"a": dev((4, 64), torch.int8), "a_scale": dev((4,), torch.float32), "b": dev((8, 64), torch.int8),
+            "b_scale": dev((8,), torch.float32), "bias": dev((8,), torch.float32), "out": dev((4, 8))}
+    args[name] = 0.5
+    with pytest.raises(ValueError, match=name):
+        moe.moe_int8_matmul(**args)
