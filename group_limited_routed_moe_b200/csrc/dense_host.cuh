@@ -6,6 +6,30 @@
 
 namespace {
 
+int64_t div_up(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// A call's memory: what it writes must not overlap what it reads, nor one
+// another (kernels read ahead, and a block writes while others still read).
+struct Span {
+  const void* p;
+  int64_t bytes;
+};
+bool overlap(const Span& a, const Span& b) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+  return x && y && x < y + static_cast<uintptr_t>(b.bytes) && y < x + static_cast<uintptr_t>(a.bytes);
+}
+bool apart(std::initializer_list<Span> outs, std::initializer_list<Span> ins) {
+  for (auto o = outs.begin(); o != outs.end(); ++o) {
+    for (auto other = outs.begin(); other != o; ++other)
+      if (overlap(*o, *other)) return false;
+    for (const Span& i : ins)
+      if (overlap(*o, i)) return false;
+  }
+  return true;
+}
+// apart, or in the same place
+bool apart_or_same(const Span& out, const Span& in) { return out.p == in.p || !overlap(out, in); }
+
 // ---- norm ------------------------------------------------------------------------
 bool type16(int t) { return t == MOE_TYPE_BF16 || t == MOE_TYPE_F16; }
 
@@ -191,8 +215,6 @@ int launch_cluster(const char* what, void (*kernel)(A), unsigned grid, int threa
   if (e != cudaSuccess) return cuda_fail(e, what);
   return MOE_OK;
 }
-
-int64_t div_up(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // Tile width and pairs per tile of a launch on CTA pairs, and its estimated
 // time in nanoseconds.
@@ -454,6 +476,13 @@ int moe_add_rmsnorm(const void* x, const void* residual, const void* weight, flo
   REQUIRE(aligned(x, 16) && aligned(out, 16) && aligned(residual, 16) && aligned(weight, 16) &&
               aligned(stream_out, 16) && aligned(scales, 16),
           "pointers must be 16-byte aligned");
+  const int64_t row = T * H * 2;
+  const Span X{x, row}, R{residual, row}, S{residual ? stream_out : nullptr, row};
+  const Span O{out, format == MOE_FORMAT_SAME ? row : T * H};
+  const Span C{format == MOE_FORMAT_SAME ? nullptr : scales, T * (group ? div_up(H, group) : 1) * 4};
+  REQUIRE(apart({O, S, C}, {{weight, H * 2}}) && apart({C}, {X, R}) && apart_or_same(S, X) && apart_or_same(S, R) &&
+              (format == MOE_FORMAT_SAME ? apart_or_same(O, X) && apart_or_same(O, R) : apart({O}, {X, R})),
+          "outputs overlap inputs or one another");
   rc = device_setup(nullptr, nullptr);
   if (rc) return rc;
   return do_add_rmsnorm(dtype, format, T, x, residual, weight, eps, static_cast<int>(H), group, stream_out, out,
@@ -482,6 +511,9 @@ int moe_add_rmsnorm_backward(const void* dy, const void* s, const void* weight, 
     return fail(MOE_ERR_WORKSPACE, "moe_add_rmsnorm_backward workspace needs %zu bytes, got %zu", need,
                 workspace ? workspace_bytes : size_t(0));
   if (T == 0 && !dweight) return MOE_OK;
+  REQUIRE(apart({{dx, T * H * 2}, {dweight, H * 4}, {dweight ? workspace : nullptr, int64_t(need)}},
+                {{dy, T * H * 2}, {s, T * H * 2}, {weight, H * 2}, {dstream, T * H * 2}}),
+          "outputs or the workspace overlap inputs or one another");
   rc = device_setup(nullptr, nullptr);
   if (rc) return rc;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
@@ -517,6 +549,9 @@ int moe_int8_matmul(const int8_t* a, const float* a_scale, const int8_t* b, cons
   REQUIRE(aligned(a, 16) && aligned(a_scale, 16) && aligned(b, 16) && aligned(b_scale, 16) && aligned(bias, 16) &&
               aligned(out, 16),
           "pointers must be 16-byte aligned");
+  REQUIRE(apart({{out, T * N * (out_dtype == MOE_TYPE_F32 ? 4 : 2)}},
+                {{a, T * K}, {a_scale, T * 4}, {b, N * K}, {b_scale, N * 4}, {bias, N * 4}}),
+          "the output overlaps an input");
   DeviceInfo dev;
   rc = device_info(&dev);
   if (rc) return rc;
@@ -546,6 +581,11 @@ int moe_gated_ffn(const void* x, const void* w_gate, const void* w_up, const voi
   REQUIRE(aligned(x, 16) && aligned(w_gate, 16) && aligned(w_up, 16) && aligned(w_down, 16) && aligned(h, 16) &&
               aligned(saved, 16) && aligned(y, 16) && aligned(residual, 16),
           "pointers must be 16-byte aligned");
+  const int64_t row = T * H * 2, w = H * I * 2;
+  const Span X{x, row}, R{residual, row}, Y{y, row}, A{h, T * I * 2}, V{saved, dense::saved_bytes(T, I)};
+  REQUIRE(apart({Y, A, V}, {{w_gate, w}, {w_up, w}, {w_down, w}}) && apart({A, V}, {X, R}) && apart_or_same(Y, X) &&
+              apart_or_same(Y, R),
+          "outputs overlap inputs or one another");
   DeviceInfo dev;
   rc = device_info(&dev);
   if (rc) return rc;
@@ -601,6 +641,11 @@ int moe_gated_ffn_backward(const void* dy, const void* x, const void* w_gate, co
   if (need && (workspace == nullptr || workspace_bytes < need))
     return fail(MOE_ERR_WORKSPACE, "moe_gated_ffn_backward workspace needs %zu bytes, got %zu", need,
                 workspace ? workspace_bytes : size_t(0));
+  const int64_t row = T * H * 2, w = H * I * 2;
+  REQUIRE(apart({{dx, row}, {dw_gate, w}, {dw_up, w}, {dw_down, w}, {need_d ? workspace : nullptr, int64_t(need)}},
+                {{dy, row}, {x, row}, {w_gate, w}, {w_up, w}, {w_down, w}, {h, T * I * 2},
+                 {saved, dense::saved_bytes(T, I)}}),
+          "outputs or the workspace overlap inputs or one another");
   rc = device_info(&dev);
   if (rc) return rc;
   char* dg = static_cast<char*>(workspace);
@@ -663,6 +708,17 @@ int moe_layer_normed(const moe_bf16* x, const moe_bf16* residual, const moe_bf16
   REQUIRE(aligned(packed_w, 128) && aligned(packed_router, 128), "packed weights must be 128-byte aligned");
   REQUIRE(aligned(bias, 16) && aligned(out, 16) && aligned(topk_idx_out, 16) && aligned(topk_w_out, 16),
           "pointers must be 16-byte aligned");
+  const int64_t row = T * kH * 2;
+  const Span X{x, row}, R{residual, row}, S{residual ? stream_out : nullptr, row}, O{out, row};
+  const Span I{topk_idx_out, T * kTopK * 4}, W{topk_w_out, T * kTopK * 4};
+  const Span weights[] = {{norm_weight, kH * 2},
+                          {packed_router, static_cast<int64_t>(moe_router_packed_bytes())},
+                          {bias, kE * 4},
+                          {packed_w, static_cast<int64_t>(moe_packed_weight_bytes())}};
+  bool ok = apart({I, W, {workspace, static_cast<int64_t>(need)}}, {X, R, S, O}) && apart_or_same(S, X) &&
+            apart_or_same(S, R) && apart_or_same(O, X) && apart_or_same(O, R) && apart_or_same(O, S);
+  for (const Span& w : weights) ok = ok && apart({w}, {I, W, S, O, {workspace, static_cast<int64_t>(need)}});
+  REQUIRE(ok, "outputs or the workspace overlap inputs or one another");
   const size_t layer = align_up(layer_ws(T, false, 0).total, 1024);
   moe_bf16* n = reinterpret_cast<moe_bf16*>(static_cast<char*>(workspace) + layer);
   rc = moe_add_rmsnorm(x, residual, norm_weight, eps, T, kH, MOE_TYPE_BF16, stream_out, MOE_FORMAT_SAME, 0, n,

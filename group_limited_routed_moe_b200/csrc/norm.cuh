@@ -187,7 +187,7 @@ __device__ __forceinline__ float row_scale(float amax, float eps) {
 template <typename E, int VEC, int NV, int FMT, int MAXT>
 __global__ void __launch_bounds__(MAXT)
     add_rmsnorm_kernel(const E* x, const E* res, const E* __restrict__ w, float eps, int H,
-                       int group, E* s_out, void* __restrict__ out, float* __restrict__ scales) {
+                       int group, E* s_out, void* out, float* __restrict__ scales) {
   __shared__ float red[3][32];
   __shared__ unsigned gmax[VEC == 1 ? kMaxH / kGroup : 1];
   using P = Pack<E, VEC>;
@@ -197,7 +197,7 @@ __global__ void __launch_bounds__(MAXT)
   const int nvec = H / VEC;
   float v[NV][VEC];
   float ss = 0.f;
-  // every load of the row before its first store (s_out may be x or res)
+  // every load of the row before its first store (s_out or out may be x or res)
   P xa[NV], ra[NV];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {

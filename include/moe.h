@@ -635,7 +635,10 @@ int moe_permute_fixed_scratch(const int32_t* topk_idx, int64_t T, int32_t* count
  * with the residual stream's addition and norm, and the model's first layer is
  * dense ("Ling-3.0-tiny on a Qualcomm board", TensorFold issue #1247, first
  * comment: dense layer 0).  Sizes are arguments here; arrays are dense
- * row-major and 16-byte aligned.  An element type is one of these codes. */
+ * row-major and 16-byte aligned.  What a call writes may overlap neither what
+ * it reads nor one another, but where an entry point says that an output may
+ * be an input (that is, in the same place); other calls are refused.  An
+ * element type is one of these codes. */
 typedef enum moe_type { MOE_TYPE_BF16 = 0, MOE_TYPE_F16 = 1, MOE_TYPE_F32 = 2 } moe_type;
 
 /* Output of moe_add_rmsnorm: the input's type, or 8-bit codes with scales. */
@@ -651,7 +654,8 @@ typedef enum moe_format { MOE_FORMAT_SAME = 0, MOE_FORMAT_INT8 = 1, MOE_FORMAT_E
  *   weight      : [H] of `dtype`, or NULL for ones
  *   stream_out  : [T][H] (out), s; required with residual, not written without.
  *                 May be x or residual.
- *   format      : MOE_FORMAT_SAME: out [T][H] of `dtype`, scales not used;
+ *   format      : MOE_FORMAT_SAME: out [T][H] of `dtype`, scales not used; out
+ *                 may be x or residual if stream_out is not;
  *                 MOE_FORMAT_INT8: out [T][H] int8 in [-127, 127];
  *                 MOE_FORMAT_E4M3: out [T][H] FP8 E4M3 (at most +-448).
  *   group       : 0, or 128 (8-bit formats): columns that share a scale, 0 the
@@ -673,7 +677,7 @@ size_t moe_add_rmsnorm_backward_workspace_bytes(int64_t T, int64_t H);
  *   dstream : [T][H] gradient that reaches s from elsewhere, added; or NULL
  *   dx      : [T][H] (out) gradient of s, which is that of x and of residual
  *   dweight : fp32 [H] (out), or NULL.  Summed in a fixed order.
- * dy, s, weight, dstream and dx are of `dtype`; dx must alias no input.
+ * dy, s, weight, dstream and dx are of `dtype`.
  * T == 0 sets dweight to zero.  With eps = 0 a row of zeros has no gradient: its
  * dx is NaN, and so is dweight. */
 int moe_add_rmsnorm_backward(const void* dy, const void* s, const void* weight, float eps, int64_t T,
@@ -719,9 +723,8 @@ size_t moe_gated_ffn_backward_workspace_bytes(int64_t T, int64_t I);
  *   dw_gate = x^T dg, dw_up = x^T du, dw_down = h^T dy
  * h and saved from the forward call; outputs of `dtype`, shapes as the inputs',
  * each may be NULL (not computed).  Inputs that no wanted output needs may be
- * NULL, and the workspace when dw_down alone is wanted.  No output may alias
- * an input or the workspace.  Every sum in a fixed order.  T == 0 sets the
- * weights' gradients to zero. */
+ * NULL, and the workspace when dw_down alone is wanted.  Every sum in a fixed
+ * order.  T == 0 sets the weights' gradients to zero. */
 int moe_gated_ffn_backward(const void* dy, const void* x, const void* w_gate, const void* w_up,
                            const void* w_down, const void* h, const void* saved, int64_t T, int64_t H,
                            int64_t I, int dtype, void* dx, void* dw_gate, void* dw_up, void* dw_down,
