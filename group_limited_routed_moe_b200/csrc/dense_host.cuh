@@ -216,10 +216,12 @@ int launch_cluster(const char* what, void (*kernel)(A), unsigned grid, int threa
   return MOE_OK;
 }
 
-// Tile width and pairs per tile of a launch on CTA pairs, and its estimated
-// time in nanoseconds.
-struct PairShape {
-  int bn, split;
+// How a launch runs.  On CTA pairs: tiles of 256 rows x `tile` columns, `split`
+// pairs to a tile.  For few tokens: tiles of `tile` tokens x `rows` weight rows,
+// `split` CTAs to a tile.  ns: the estimated time of a launch on CTA pairs.
+struct Plan {
+  bool pairs;
+  int tile, rows, split;
   int64_t ns;
 };
 
@@ -231,8 +233,8 @@ struct PairShape {
 // 14.2, by four 24 (two rounds of clusters); 32 tiles of 128 columns 15.0,
 // shared by two 11.6.
 template <int EPI>
-PairShape pair_shape(const Product& p, int64_t kbs, const DeviceInfo& dev) {
-  PairShape best{256, 1, INT64_MAX};
+Plan pair_plan(const Product& p, int64_t kbs, const DeviceInfo& dev) {
+  Plan best{true, 256, dense::kBM, 1, INT64_MAX};
   for (const int bn : {256, 128}) {
     int64_t tiles = 0;
     for (int i = 0; i < p.nprob; ++i)
@@ -243,7 +245,7 @@ PairShape pair_shape(const Product& p, int64_t kbs, const DeviceInfo& dev) {
       const int64_t rounds = split > 1 ? 1 : div_up(tiles, dev.sms / 2);
       const int64_t share = split == 1 ? 0 : bn == 256 ? 2200 : 900 + 600 * (split - 2);
       const int64_t ns = rounds * div_up(kbs, split) * (bn == 256 ? 300 : 290) + (bn == 256 ? 6500 : 5000) + share;
-      if (ns < best.ns) best = {bn, split, ns};
+      if (ns < best.ns) best = {true, bn, dense::kBM, split, ns};
     }
   }
   return best;
@@ -256,14 +258,13 @@ int64_t all_kblocks(const Product& p) {
 }
 
 template <int KIND, bool A_MN, bool B_MN, int EPI>
-int launch_pair(const Product& p, const DeviceInfo& dev, cudaStream_t s) {
+int launch_pair(const Product& p, const Plan& plan, const DeviceInfo& dev, cudaStream_t s) {
   const int elem = KIND == dense::kI8Kind ? 1 : 2, ke = 128 / elem;
   dense::Args g{};
   g.nseg = p.nseg;
   g.kblocks = static_cast<int>(div_up(p.a[0].k(), ke));
-  const PairShape shape = pair_shape<EPI>(p, all_kblocks<KIND>(p), dev);
-  const int bn = shape.bn;
-  g.split = shape.split;
+  const int bn = plan.tile;
+  g.split = plan.split;
   int64_t tiles = 0;
   const int out_elem = p.type == dense::kF32 ? 4 : 2;
   g.tma_out = true;  // unless some product's rows are not whole 16-byte pieces
@@ -312,7 +313,7 @@ int small_split(int64_t tiles, int64_t kbs, int64_t room) {
 }
 
 template <int KIND, bool W_MN, int EPI, int NT, int ROWS>
-int launch_small_rows(const Product& p, int sms, cudaStream_t s) {
+int launch_small_rows(const Product& p, int split, cudaStream_t s) {
   const int elem = KIND == dense::kI8Kind ? 1 : 2, ke = 128 / elem;
   dense::SmallArgs g{};
   g.T = p.a[0].outer();
@@ -330,7 +331,7 @@ int launch_small_rows(const Product& p, int sms, cudaStream_t s) {
     int rc = make_map(&g.w[1], p.b[1].p, p.b[1].rows, p.b[1].cols, elem, 64);
     if (rc) return rc;
   }
-  g.split = small_split(tiles, int64_t(g.kblocks) * g.nseg, int64_t(sms) * dense::SmallCfg<NT, ROWS>::PER_SM);
+  g.split = split;
   g.out = p.out[0];
   common_args(&g, p);
   g.out2 = p.out2;
@@ -341,8 +342,14 @@ int launch_small_rows(const Product& p, int sms, cudaStream_t s) {
                         dense::SmallCfg<NT, ROWS>::SMEM, g.split, s, g);
 }
 
-template <int KIND, bool W_MN, int EPI, int NT>
-int launch_small_nt(const Product& p, int sms, cudaStream_t s) {
+template <int KIND, int EPI, int NT, int ROWS>
+Plan small_plan_rows(const Product& p, int sms) {
+  const int64_t tiles = div_up(p.b[0].outer(), EPI == dense::kGated ? 64 : ROWS) * div_up(p.a[0].outer(), NT);
+  const int64_t room = int64_t(sms) * dense::SmallCfg<NT, ROWS>::PER_SM;
+  return {false, NT, ROWS, small_split(tiles, all_kblocks<KIND>(p), room), 0};
+}
+template <int KIND, int EPI, int NT>
+Plan small_plan(const Product& p, int sms) {
   if constexpr (EPI != dense::kGated) {
     // Tiles of 64 weight rows where 128-row tiles, split as far as they go, are
     // fewer than the SMs; with more than two token tiles already where they
@@ -352,27 +359,43 @@ int launch_small_nt(const Product& p, int sms, cudaStream_t s) {
     const int64_t tiles = div_up(p.b[0].outer(), 128) * token_tiles;
     const int64_t room = token_tiles > 2 ? sms : int64_t(sms) * dense::SmallCfg<NT, 128>::PER_SM;
     if (tiles * small_split(tiles, all_kblocks<KIND>(p), room) < sms)
-      return launch_small_rows<KIND, W_MN, EPI, NT, 64>(p, sms, s);
+      return small_plan_rows<KIND, EPI, NT, 64>(p, sms);
   }
-  return launch_small_rows<KIND, W_MN, EPI, NT, 128>(p, sms, s);
+  return small_plan_rows<KIND, EPI, NT, 128>(p, sms);
 }
 
-// One product of T tokens with weights.  Up to 32 tokens the weights are the
-// MMA's rows; above, by the estimate of both ways: with the weights as rows 4 us,
-// 0.38 us for each k-block (128 weight rows x 64 tokens) and 2 us for each tile
-// that an SM gets, measured over the sizes that pair_shape names (int8, N = 4096:
-// T = 128, K = 4096 9.4 us against 11.3 on pairs, T = 256 13.0 against 11.4,
-// T = 192, K = 1536 9.4 against 8.3; N = 512, T = 256, K = 1536 4.2 against 7.7).
-template <int KIND, bool B_MN, int EPI>
-int launch_product(const Product& p, const DeviceInfo& dev, cudaStream_t s) {
+// The kernel for one product of T tokens with weights.  Up to 32 tokens the
+// weights are the MMA's rows; above, by the estimate of both ways: with the
+// weights as rows 4 us, 0.38 us for each k-block (128 weight rows x 64 tokens)
+// and 2 us for each tile that an SM gets, measured over the sizes that pair_plan
+// names (int8, N = 4096: T = 128, K = 4096 9.4 us against 11.3 on pairs, T = 256
+// 13.0 against 11.4, T = 192, K = 1536 9.4 against 8.3; N = 512, T = 256, K = 1536
+// 4.2 against 7.7).
+template <int KIND, int EPI>
+Plan product_plan(const Product& p, const DeviceInfo& dev) {
   const int64_t T = p.a[0].outer();
-  if (T <= 16) return launch_small_nt<KIND, B_MN, EPI, 16>(p, dev.sms, s);
-  if (T <= 32) return launch_small_nt<KIND, B_MN, EPI, 32>(p, dev.sms, s);
+  if (T <= 16) return small_plan<KIND, EPI, 16>(p, dev.sms);
+  if (T <= 32) return small_plan<KIND, EPI, 32>(p, dev.sms);
   const int64_t tiles = div_up(p.b[0].outer(), EPI == dense::kGated ? 64 : 128) * div_up(T, 64);
   const int64_t kbs = all_kblocks<KIND>(p);
-  if (4000 + tiles * (kbs * 380 + 2000) / dev.sms <= pair_shape<EPI>(p, kbs, dev).ns)
-    return launch_small_nt<KIND, B_MN, EPI, 64>(p, dev.sms, s);
-  return launch_pair<KIND, false, B_MN, EPI>(p, dev, s);
+  const Plan pairs = pair_plan<EPI>(p, kbs, dev);
+  return 4000 + tiles * (kbs * 380 + 2000) / dev.sms <= pairs.ns ? small_plan<KIND, EPI, 64>(p, dev.sms) : pairs;
+}
+
+template <int KIND, bool W_MN, int EPI, int NT>
+int launch_small(const Product& p, const Plan& plan, cudaStream_t s) {
+  if constexpr (EPI != dense::kGated)
+    if (plan.rows == 64) return launch_small_rows<KIND, W_MN, EPI, NT, 64>(p, plan.split, s);
+  return launch_small_rows<KIND, W_MN, EPI, NT, 128>(p, plan.split, s);
+}
+
+template <int KIND, bool B_MN, int EPI>
+int launch_product(const Product& p, const DeviceInfo& dev, cudaStream_t s) {
+  const Plan plan = product_plan<KIND, EPI>(p, dev);
+  if (plan.pairs) return launch_pair<KIND, false, B_MN, EPI>(p, plan, dev, s);
+  if (plan.tile == 16) return launch_small<KIND, B_MN, EPI, 16>(p, plan, s);
+  if (plan.tile == 32) return launch_small<KIND, B_MN, EPI, 32>(p, plan, s);
+  return launch_small<KIND, B_MN, EPI, 64>(p, plan, s);
 }
 
 template <int KIND, bool A_MN, bool B_MN, int EPI>
@@ -438,6 +461,48 @@ cudaError_t dense_setup(DeviceInfo* dev) {
   return e;
 }
 
+// The gated block's products, by their sizes; the entry points add the rest.
+Product gate_up_product(int64_t T, int64_t H, int64_t I) {
+  Product p{};
+  p.a[0] = {nullptr, T, H, false};
+  p.b[0] = p.b[1] = {nullptr, H, I, true};
+  return p;
+}
+Product down_product(int64_t T, int64_t H, int64_t I) {
+  Product p{};
+  p.a[0] = {nullptr, T, I, false};
+  p.b[0] = {nullptr, I, H, true};
+  return p;
+}
+Product dh_product(int64_t T, int64_t H, int64_t I) {
+  Product p{};
+  p.a[0] = {nullptr, T, H, false};
+  p.b[0] = {nullptr, I, H, false};
+  return p;
+}
+Product dx_product(int64_t T, int64_t H, int64_t I) {
+  Product p{};
+  p.a[0] = p.a[1] = {nullptr, T, I, false};
+  p.b[0] = p.b[1] = {nullptr, H, I, false};
+  p.nseg = 2;
+  return p;
+}
+Product dw_product(int64_t T, int64_t H, int64_t I) {
+  Product p{};
+  p.a[0] = p.a[1] = {nullptr, T, H, true};
+  p.a[2] = {nullptr, T, I, true};
+  p.b[0] = p.b[1] = {nullptr, T, I, true};
+  p.b[2] = {nullptr, T, H, true};
+  p.nprob = 3;
+  return p;
+}
+Product int8_product(int64_t T, int64_t N, int64_t K) {
+  Product p{};
+  p.a[0] = {nullptr, T, K, false};
+  p.b[0] = {nullptr, N, K, false};
+  return p;
+}
+
 int check_ffn(int64_t T, int64_t H, int64_t I, int dtype) {
   int rc = check_T(T);
   if (rc) return rc;
@@ -445,6 +510,14 @@ int check_ffn(int64_t T, int64_t H, int64_t I, int dtype) {
           "H=%lld and I=%lld must be multiples of 8 in [8, %lld]", static_cast<long long>(H),
           static_cast<long long>(I), static_cast<long long>(kMaxDim));
   REQUIRE(type16(dtype), "dtype=%d: bf16 or fp16", dtype);
+  return MOE_OK;
+}
+
+int check_int8(int64_t N, int64_t K) {
+  REQUIRE(N >= 1 && N <= kMaxInt8N, "N=%lld outside [1, %lld]", static_cast<long long>(N),
+          static_cast<long long>(kMaxInt8N));
+  REQUIRE(K >= 16 && K <= kMaxInt8K && K % 16 == 0, "K=%lld must be a multiple of 16 in [16, %lld]",
+          static_cast<long long>(K), static_cast<long long>(kMaxInt8K));
   return MOE_OK;
 }
 
@@ -539,10 +612,8 @@ int moe_int8_matmul(const int8_t* a, const float* a_scale, const int8_t* b, cons
                     moe_stream_t stream) {
   int rc = check_T(T);
   if (rc) return rc;
-  REQUIRE(N >= 1 && N <= kMaxInt8N, "N=%lld outside [1, %lld]", static_cast<long long>(N),
-          static_cast<long long>(kMaxInt8N));
-  REQUIRE(K >= 16 && K <= kMaxInt8K && K % 16 == 0, "K=%lld must be a multiple of 16 in [16, %lld]",
-          static_cast<long long>(K), static_cast<long long>(kMaxInt8K));
+  rc = check_int8(N, K);
+  if (rc) return rc;
   REQUIRE(type16(out_dtype) || out_dtype == MOE_TYPE_F32, "out_dtype=%d: bf16, fp16 or fp32", out_dtype);
   if (T == 0) return MOE_OK;
   REQUIRE(a && a_scale && b && b_scale && out, "null pointer");
@@ -555,9 +626,9 @@ int moe_int8_matmul(const int8_t* a, const float* a_scale, const int8_t* b, cons
   DeviceInfo dev;
   rc = device_info(&dev);
   if (rc) return rc;
-  Product p{};
-  p.a[0] = {a, T, K, false};
-  p.b[0] = {b, N, K, false};
+  Product p = int8_product(T, N, K);
+  p.a[0].p = a;
+  p.b[0].p = b;
   p.out[0] = out;
   p.type = out_dtype;
   p.a_scale = a_scale;
@@ -590,18 +661,18 @@ int moe_gated_ffn(const void* x, const void* w_gate, const void* w_up, const voi
   rc = device_info(&dev);
   if (rc) return rc;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  Product up{};
-  up.a[0] = {x, T, H, false};
-  up.b[0] = {w_gate, H, I, true};
-  up.b[1] = {w_up, H, I, true};
+  Product up = gate_up_product(T, H, I);
+  up.a[0].p = x;
+  up.b[0].p = w_gate;
+  up.b[1].p = w_up;
   up.out[0] = h;
   up.type = dtype;
   up.saved = saved;
   rc = launch_product<dense::kF16Kind, true, dense::kGated>(up, dev, s);
   if (rc) return rc;
-  Product down{};
-  down.a[0] = {h, T, I, false};
-  down.b[0] = {w_down, I, H, true};
+  Product down = down_product(T, H, I);
+  down.a[0].p = h;
+  down.b[0].p = w_down;
   down.out[0] = y;
   down.type = dtype;
   down.residual = residual;
@@ -651,9 +722,9 @@ int moe_gated_ffn_backward(const void* dy, const void* x, const void* w_gate, co
   char* dg = static_cast<char*>(workspace);
   char* du = dg + static_cast<size_t>(T) * static_cast<size_t>(I) * 2;
   if (need_d) {
-    Product p{};
-    p.a[0] = {dy, T, H, false};
-    p.b[0] = {w_down, I, H, false};
+    Product p = dh_product(T, H, I);
+    p.a[0].p = dy;
+    p.b[0].p = w_down;
     p.out[0] = dg;
     p.out2 = du;
     p.type = dtype;
@@ -662,12 +733,11 @@ int moe_gated_ffn_backward(const void* dy, const void* x, const void* w_gate, co
     if (rc) return rc;
   }
   if (dx) {
-    Product p{};
-    p.a[0] = {dg, T, I, false};
-    p.a[1] = {du, T, I, false};
-    p.b[0] = {w_gate, H, I, false};
-    p.b[1] = {w_up, H, I, false};
-    p.nseg = 2;
+    Product p = dx_product(T, H, I);
+    p.a[0].p = dg;
+    p.a[1].p = du;
+    p.b[0].p = w_gate;
+    p.b[1].p = w_up;
     p.out[0] = dx;
     p.type = dtype;
     rc = launch_product<dense::kF16Kind, false, dense::kPlain>(p, dev, s);
@@ -676,15 +746,50 @@ int moe_gated_ffn_backward(const void* dy, const void* x, const void* w_gate, co
   // The weights' gradients asked for, in one launch, whose shape goes by all
   // three: a gradient's bits do not depend on which others are wanted.
   if (!dw_gate && !dw_up && !dw_down) return MOE_OK;
-  Product p{};
-  p.nprob = 3;
+  Product p = dw_product(T, H, I);
   p.type = dtype;
   for (int i = 0; i < 3; ++i) {
-    p.a[i] = i < 2 ? Operand{x, T, H, true} : Operand{h, T, I, true};
-    p.b[i] = i < 2 ? Operand{i == 0 ? dg : du, T, I, true} : Operand{dy, T, H, true};
+    p.a[i].p = i < 2 ? x : h;
+    p.b[i].p = i == 0 ? dg : i == 1 ? du : dy;
     p.out[i] = dw[i];
   }
-  return launch_pair<dense::kF16Kind, true, true, dense::kPlain>(p, dev, s);
+  const Plan plan = pair_plan<dense::kPlain>(p, all_kblocks<dense::kF16Kind>(p), dev);
+  return launch_pair<dense::kF16Kind, true, true, dense::kPlain>(p, plan, dev, s);
+}
+
+// ---- how a product runs --------------------------------------------------------------
+int moe_dense_plan(int product, int64_t T, int64_t N, int64_t K, int32_t* plan) {
+  const bool int8 = product == MOE_PRODUCT_INT8;
+  int rc = check_T(T);
+  if (!rc) rc = int8 ? check_int8(N, K) : check_ffn(T, K, N, MOE_TYPE_BF16);
+  if (rc) return rc;
+  REQUIRE(T > 0 && plan, "T=%lld: there is no product", static_cast<long long>(T));
+  DeviceInfo dev;
+  if (device_info(&dev) != MOE_OK) {  // no device here: a B200's
+    dev.sms = 148;
+    const int clusters[dense::kMaxPairs + 1] = {0, 0, 33, 22, 15};
+    std::copy(clusters, clusters + dense::kMaxPairs + 1, dev.clusters);
+  }
+  using namespace dense;
+  Plan r{};
+  switch (product) {
+    case MOE_PRODUCT_GATE_UP: r = product_plan<kF16Kind, kGated>(gate_up_product(T, K, N), dev); break;
+    case MOE_PRODUCT_DOWN: r = product_plan<kF16Kind, kPlain>(down_product(T, K, N), dev); break;
+    case MOE_PRODUCT_DH: r = product_plan<kF16Kind, kDGate>(dh_product(T, K, N), dev); break;
+    case MOE_PRODUCT_DX: r = product_plan<kF16Kind, kPlain>(dx_product(T, K, N), dev); break;
+    case MOE_PRODUCT_DW: {
+      const Product p = dw_product(T, K, N);
+      r = pair_plan<kPlain>(p, all_kblocks<kF16Kind>(p), dev);
+      break;
+    }
+    case MOE_PRODUCT_INT8: r = product_plan<kI8Kind, kScaled>(int8_product(T, N, K), dev); break;
+    default: return fail(MOE_ERR_INVALID_ARG, "product=%d", product);
+  }
+  plan[0] = r.pairs;
+  plan[1] = r.tile;
+  plan[2] = r.rows;
+  plan[3] = r.split;
+  return MOE_OK;
 }
 
 // ---- the pre-norm layer ------------------------------------------------------------

@@ -104,6 +104,7 @@ _SIGS = {
     "moe_gated_ffn": ([_p, _p, _p, _p, _i64, _i64, _i64, _i32, _p, _p, _p, _p, _p], _i32),
     "moe_gated_ffn_backward_workspace_bytes": ([_i64, _i64], _sz),
     "moe_gated_ffn_backward": ([_p] * 7 + [_i64, _i64, _i64, _i32] + [_p] * 5 + [_sz, _p], _i32),
+    "moe_dense_plan": ([_i32, _i64, _i64, _i64, _p], _i32),
     "moe_layer_normed_workspace_bytes": ([_i64], _sz),
     "moe_layer_normed": ([_p, _p, _p, _f32, _p, _p, _p, _i64, _p, _p, _p, _p, _p, _sz, _p], _i32),
 }
@@ -1018,6 +1019,17 @@ def moe_gated_ffn_backward(dy: torch.Tensor, x: torch.Tensor, w_gate: torch.Tens
     if rc:
         _check("moe_gated_ffn_backward", rc)
     return dx, dw_gate, dw_up, dw_down
+
+
+PRODUCTS = ("gate_up", "down", "dh", "dx", "dw", "int8")
+
+
+def dense_plan(product: str, T: int, N: int, K: int) -> tuple[str, int, int, int]:
+    """How a dense product runs (see include/moe.h, moe_dense_plan): ("pairs",
+    columns, rows, split) or ("few", tokens, weight rows, split)."""
+    plan = (ctypes.c_int32 * 4)()
+    _check("moe_dense_plan", lib.moe_dense_plan(PRODUCTS.index(product), T, N, K, plan))
+    return ("pairs" if plan[0] else "few", plan[1], plan[2], plan[3])
 
 
 def layer_normed_workspace_bytes(T: int) -> int:

@@ -730,6 +730,19 @@ int moe_gated_ffn_backward(const void* dy, const void* x, const void* w_gate, co
                            int64_t I, int dtype, void* dx, void* dw_gate, void* dw_up, void* dw_down,
                            void* workspace, size_t workspace_bytes, moe_stream_t stream);
 
+/* Diagnostic: how the current device (where there is none, a B200) runs one of
+ * the products above.  Host only, nothing is launched.
+ *   product : gate/up, down, dh, dx or the weights' gradients of the gated block
+ *             with H = K and I = N, or the int8 product
+ *   plan    : int32 [4] (out): 1 on CTA pairs, 0 with the weights as the MMA's
+ *             rows; the tile's columns (pairs) or tokens; its rows; the pairs or
+ *             CTAs that share a tile by k */
+typedef enum moe_product {
+  MOE_PRODUCT_GATE_UP = 0, MOE_PRODUCT_DOWN = 1, MOE_PRODUCT_DH = 2, MOE_PRODUCT_DX = 3, MOE_PRODUCT_DW = 4,
+  MOE_PRODUCT_INT8 = 5
+} moe_product;
+int moe_dense_plan(int product, int64_t T, int64_t N, int64_t K, int32_t* plan);
+
 /* Workspace bytes moe_layer_normed needs: moe_layer's, and the normed rows. */
 size_t moe_layer_normed_workspace_bytes(int64_t T);
 
