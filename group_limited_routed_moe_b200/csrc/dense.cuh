@@ -264,11 +264,14 @@ __device__ __forceinline__ float unpack1(uint16_t v, int type) {
   return type == kF16 ? __half2float(__ushort_as_half(v)) : __uint_as_float(uint32_t(v) << 16);
 }
 
-// 1 / (1 + e^-g) by the approximate exponential and reciprocal (2^-21 together;
-// the 16-bit rounding that follows is 2^-11 at best), results below 2^-126
-// flushed: without the flush their range handling was half of the epilogues'
-// instructions.  For very negative g the exponential is infinite and the
-// quotient 0, the limit.
+// 1 / (1 + e^-g) by the approximate exponential and reciprocal.  Relative error
+// below 2^-21 (exponential 2^-22, sum 2^-24, reciprocal 2^-23) and, where
+// e^-g counts, 1.25 |g| 2^-24 more: g log2(e) is rounded (2^-24 of it, the
+// constant 2^-26), an absolute error of the exponent.  At g = -16 that is 2^-19.4
+// together, where the 16-bit rounding that follows is 2^-11 at best.  Results
+// below 2^-126 are flushed: without the flush their range handling was half of the
+// epilogues' instructions.  For very negative g the exponential is infinite and
+// the quotient 0, the limit.
 __device__ __forceinline__ float sigmoid(float g) {
   float e, r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950408889634f));
