@@ -16,6 +16,9 @@
 // MN-major one is chunks of 64 m (or n), each 64 k-rows of 128 bytes, same
 // swizzle.  TMA fills what lies outside the matrix with zeros, in both
 // operands, so ragged sizes need no masks before the store.
+// h, dg and du go from one product to the next rounded to 16 bits, the tensor
+// cores' operands (fp32 ones would have to be split into two or three 16-bit
+// products); the sums before the rounding are fp32.
 //
 // pair_gemm_kernel: two CTAs of a cluster work on one 256 x BN tile
 // (tcgen05.mma.cta_group::2): each loads 128 rows of A and BN/2 rows of B and
@@ -267,7 +270,7 @@ __device__ __forceinline__ float unpack1(uint16_t v, int type) {
 // 1 / (1 + e^-g) by the approximate exponential and reciprocal.  Relative error
 // below 2^-21 (exponential 2^-22, sum 2^-24, reciprocal 2^-23) and, where
 // e^-g counts, 1.25 |g| 2^-24 more: g log2(e) is rounded (2^-24 of it, the
-// constant 2^-26), an absolute error of the exponent.  At g = -16 that is 2^-19.4
+// constant 2^-26), an absolute error of the exponent.  At g = -16 that is 2^-19.2
 // together, where the 16-bit rounding that follows is 2^-11 at best.  Results
 // below 2^-126 are flushed: without the flush their range handling was half of the
 // epilogues' instructions.  For very negative g the exponential is infinite and

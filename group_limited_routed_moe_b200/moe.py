@@ -774,6 +774,8 @@ class HostPipeline:
 
 
 # ----------------------------------------------------------------- norm and dense products
+# Calls of the library, not recorded by torch's autograd: outputs carry no graph,
+# also where inputs require gradients; the backward passes are calls of their own.
 
 _TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 NORM_FORMATS = {"same": 0, "int8": 1, "e4m3": 2}

@@ -664,7 +664,8 @@ typedef enum moe_format { MOE_FORMAT_SAME = 0, MOE_FORMAT_INT8 = 1, MOE_FORMAT_E
  *                 2^-126), top 127 or 448; a value is code * scale, codes are
  *                 rounded to nearest.  A NaN makes all its row's scales NaN; an
  *                 infinity its own group's (its row's others have values 0).
- * 1 <= H <= 32768; rows of H % 8 == 0 take 16-byte accesses. */
+ * 1 <= H <= 32768; rows of H % 8 == 0 take 16-byte accesses, others 2-byte
+ * ones; the backward pass is at its best up to H = 8192. */
 int moe_add_rmsnorm(const void* x, const void* residual, const void* weight, float eps, int64_t T,
                     int64_t H, int dtype, void* stream_out, int format, int group, void* out,
                     float* scales, moe_stream_t stream);
@@ -708,7 +709,12 @@ size_t moe_gated_ffn_saved_bytes(int64_t T, int64_t I);
  *   residual : [T][H] or NULL;  h : [T][I] (out);  y : [T][H] (out)
  *   saved    : moe_gated_ffn_saved_bytes(T, I) bytes (out), or NULL when no
  *              backward pass follows
- * y may be x or residual.  H and I multiples of 8 in [8, 65536]. */
+ * y may be x or residual.  H and I multiples of 8 in [8, 65536].
+ * h, and dg and du of the backward pass, are rounded to `dtype`, which the next
+ * product reads: in fp16 an h above 65504 becomes infinite, and gradients below
+ * 2^-14 lose digits, below 2^-25 vanish (scale the loss, or take bf16).  The
+ * order of a token's sums depends on T, so its last bits may differ between
+ * batches (moe_layer's do not); they do not differ between calls. */
 int moe_gated_ffn(const void* x, const void* w_gate, const void* w_up, const void* w_down, int64_t T,
                   int64_t H, int64_t I, int dtype, const void* residual, void* h, void* saved, void* y,
                   moe_stream_t stream);
