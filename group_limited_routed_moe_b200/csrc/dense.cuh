@@ -349,6 +349,7 @@ __device__ __forceinline__ void store_block(const uint32_t* pk, uint32_t stage, 
 
 // The same for rows that are not 16-byte aligned, element by element (of ES
 // bytes), lanes along the row; nrows rows and ncols columns of the block exist.
+// (int8, T = 8189, K = 1536, bf16: 131 us with N = 8191, 90 with 8192.)
 template <int ES>
 __device__ __forceinline__ void store_block_ragged(const uint32_t* pk, uint32_t block, uint8_t* g0, int64_t ld_bytes,
                                                    int nrows, int64_t ncols, int lane) {
